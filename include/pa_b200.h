@@ -75,6 +75,8 @@ extern "C" {
 #define PA_DEV_ERR_PLAN 0x40u       /* a cascade plan disagrees with the call: a group member's table differs on the
                                        shared prefix or its context ends inside it, or a plan index is out of range */
 
+#define PA_DEV_ERR_POSITION 0x80u   /* a positions entry >= max_positions */
+
 /* ---- build flags (pa_build_flags) ---- */
 #define PA_BUILD_DEBUG 0x1u /* built with PA_DEBUG: every derived index is checked on the device before use */
 
@@ -102,6 +104,87 @@ int pa_write_kv(const void *k, const void *v, void *k_cache, void *v_cache, cons
                 int64_t num_tokens, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                 int64_t num_blocks, int64_t k_token_stride, int64_t v_token_stride, int32_t dtype,
                 void *stream);
+
+/*
+ * pa_rope_write_kv -- pa_write_kv with the rotary position embedding applied
+ * on the way: the queries and keys of this step's tokens are turned by their
+ * positions, the turned keys and the values stored to their slots, the turned
+ * queries to q_out.  With r = rot_dim, token t at position p = positions[t],
+ * and for i < r / 2 the pair (a, b) = (i, i + r / 2), or (2 i, 2 i + 1) when
+ * `interleaved` is non-zero, each head row x becomes
+ *   x'[a] = x[a] cos_sin[p][i] - x[b] cos_sin[p][r / 2 + i]
+ *   x'[b] = x[b] cos_sin[p][i] + x[a] cos_sin[p][r / 2 + i]
+ * and keeps its dims from r on.  Arithmetic is fp32 (each product and sum
+ * rounded on its own), rounded to nearest-even into the storage type.  V rows
+ * are copied bit for bit.
+ *   q              [num_tokens][num_q_heads][head_dim], token stride
+ *                  q_token_stride; may be NULL with num_q_heads == 0.
+ *   q_out          like q, token stride q_out_token_stride; may be q itself
+ *                  (same address and stride), must not overlap it otherwise.
+ *   k, v, caches, slot_mapping  as for pa_write_kv.
+ *   positions      int64 [num_tokens].  A negative position marks padding:
+ *                  nothing is read or written for that token.  One
+ *                  >= max_positions sets PA_DEV_ERR_POSITION; the token's
+ *                  q_out rows become zeros and its K/V are not written.
+ *   cos_sin        fp32 [max_positions][rot_dim]: rot_dim / 2 cosines, then
+ *                  as many sines, 16-byte aligned.
+ *   rot_dim        a positive multiple of 16, at most head_dim.
+ * A negative slot skips the token's K/V only; a slot outside the pool sets
+ * PA_DEV_ERR_SLOT and skips them too.  num_tokens == 0 launches nothing.
+ */
+int pa_rope_write_kv(const void *q, const void *k, const void *v, void *q_out, void *k_cache, void *v_cache,
+                     const int64_t *slot_mapping, const int64_t *positions, const float *cos_sin, int64_t num_tokens,
+                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim,
+                     int32_t interleaved, int32_t block_size, int64_t num_blocks, int64_t max_positions,
+                     int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                     int64_t q_out_token_stride, int32_t dtype, void *stream);
+
+/*
+ * ---- caches held in 8 bits ----
+ *
+ * The 8-bit calls (names ending in _fp8) work on caches of e4m3 bytes (4
+ * exponent bits, 3 mantissa bits, largest value 448, no infinities; 0x7f and
+ * 0xff are NaN) in the layout of the 16-bit ones, [num_blocks][num_kv_heads]
+ * [block_size][head_dim], with one fp32 scale for each block and kv head of K
+ * (k_scale) and of V (v_scale), [num_blocks][num_kv_heads] contiguous and
+ * 4-byte aligned: a stored byte b stands for value(b) * scale.  Scales of
+ * blocks in use are finite and >= 0.  `dtype` is the type of q, k, v and out.
+ *
+ * pa_write_kv_fp8 -- quantise this step's K and V rows into their slots.
+ * Tokens of the call that lie in one block form the block's new rows; with
+ * amax the largest finite magnitude among a head's new rows there, and
+ *   want = the smallest power of two >= 2^-64 with amax <= 448 * want,
+ * the (block, head)'s scale becomes
+ *   want                   if row 0 of the block is among the new rows (the
+ *                          block starts anew: bytes of its other rows mean
+ *                          nothing until they are written),
+ *   max(scale, want)       otherwise; where this is larger than before, the
+ *                          block's bytes become rn(value(b) * old / new),
+ * and the new rows' bytes rn(x / scale), rn rounding to nearest-even e4m3.
+ * Powers of two keep the quantisation a single rounding, and re-scaled bytes
+ * exact down to e4m3's smallest normal value.  Infinite x give +-448, NaN
+ * gives NaN; neither moves the scale.
+ * slot_mapping as for pa_write_kv, and in addition the tokens of one block
+ * must stand together in it, with nothing but skipped tokens between them (a
+ * sequence's new tokens do): one warp then owns a block's scale.  Two
+ * stretches that name one block, with other blocks' tokens between, race on it.
+ */
+int pa_write_kv_fp8(const void *k, const void *v, void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                    const int64_t *slot_mapping, int64_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                    int32_t block_size, int64_t num_blocks, int64_t k_token_stride, int64_t v_token_stride,
+                    int32_t dtype, void *stream);
+
+/*
+ * pa_rope_write_kv_fp8 -- pa_rope_write_kv into an 8-bit cache: keys are
+ * turned in fp32 and quantised from there (one rounding), K and V as
+ * pa_write_kv_fp8 stores them, q_out in the storage type.  One launch.
+ */
+int pa_rope_write_kv_fp8(const void *q, const void *k, const void *v, void *q_out, void *k_cache, void *v_cache,
+                         float *k_scale, float *v_scale, const int64_t *slot_mapping, const int64_t *positions,
+                         const float *cos_sin, int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t rot_dim, int32_t interleaved, int32_t block_size,
+                         int64_t num_blocks, int64_t max_positions, int64_t q_token_stride, int64_t k_token_stride,
+                         int64_t v_token_stride, int64_t q_out_token_stride, int32_t dtype, void *stream);
 
 /*
  * pa_decode_workspace_size -- bytes of device workspace pa_decode needs for

@@ -12,6 +12,9 @@ CPU fallback: if the library is missing or no GPU is present the calls raise.
 * :func:`decode_cascade` -- the same attention for batches whose tables share
   leading blocks, each shared tile read once per group ("4. vLLM核心机制",
   section 4.2), with :func:`find_prefix_groups` and :func:`cascade_plan` on the host.
+* :func:`rope_write_kv` -- the write with the rotary position embedding applied on the way;
+  :func:`write_kv_fp8`, :func:`rope_write_kv_fp8` -- into caches held in 8 bits with a
+  scale for each block and kv head.
 
 Caches are ``[num_blocks, num_kv_heads, block_size, head_dim]`` float16 or
 bfloat16 tensors; ``block_tables`` int32 ``[S, max_blocks]``; ``context_lens``
@@ -33,7 +36,7 @@ __all__ = [
     "DEV_ERR_INTERNAL", "BUILD_DEBUG", "build_flags",
     "BlockManager", "BlockManagerError", "DecodeStepPlan", "PrefillStepPlan",
     "DEV_ERR_PLAN", "find_prefix_groups", "cascade_plan", "cascade_workspace_size", "decode_cascade", "PrefixGroups",
-    "CascadePlan",
+    "CascadePlan", "DEV_ERR_POSITION", "rope_table", "rope_write_kv", "write_kv_fp8", "rope_write_kv_fp8",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -48,6 +51,7 @@ DEV_ERR_SLOT = 0x8
 DEV_ERR_TIMEOUT = 0x10
 DEV_ERR_INTERNAL = 0x20
 DEV_ERR_PLAN = 0x40
+DEV_ERR_POSITION = 0x80
 BUILD_DEBUG = 0x1
 
 _DTYPES = {torch.float16: 1, torch.bfloat16: 2}
@@ -61,6 +65,7 @@ EXPORTED_SYMBOLS = (
     "pa_bm_is_swapped", "pa_bm_block_table", "pa_bm_slots", "pa_bm_append_slot", "pa_bm_build_decode_step", "pa_bm_build_prefill_step", "pa_bm_step_needs",
     "pa_bm_swap_out", "pa_bm_swap_in", "pa_prefill", "pa_read_bandwidth_probe", "pa_build_flags",
     "pa_find_prefix_groups", "pa_cascade_plan", "pa_cascade_workspace_size", "pa_decode_cascade",
+    "pa_rope_write_kv", "pa_write_kv_fp8", "pa_rope_write_kv_fp8",
 )
 
 
@@ -119,10 +124,12 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.pa_build_flags.argtypes = []
         lib.pa_version.restype = i32
         lib.pa_version.argtypes = []
+        from .append import bind as _bind_append
         from .block_manager import bind as _bind_block_manager
         from .cascade import bind as _bind_cascade
         _bind_block_manager(lib)
         _bind_cascade(lib)
+        _bind_append(lib)
         if path is None:
             _lib = lib
         return lib
@@ -356,5 +363,6 @@ def debug_wait_timeout(limit_ns: int = 10_000_000) -> None:
 
 
 from .block_manager import BlockManager, BlockManagerError, DecodeStepPlan, PrefillStepPlan  # noqa: E402
+from .append import rope_table, rope_write_kv, rope_write_kv_fp8, write_kv_fp8  # noqa: E402
 from .cascade import (CascadePlan, PrefixGroups, cascade_plan, cascade_workspace_size,  # noqa: E402
                       decode_cascade, find_prefix_groups)

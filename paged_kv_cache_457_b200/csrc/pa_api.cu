@@ -14,6 +14,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "pa_append.cuh"
 #include "pa_b200.h"
 #include "pa_cascade.cuh"
 #include "pa_copy.cuh"
@@ -543,9 +544,192 @@ int static_workspace_address(void **addr) {
   return PA_OK;
 }
 
+// ---- appends with rotation and into 8-bit caches (pa_append.cuh)
+
+// Checks shared by the appends; `rope`: positions, angles and q take part.
+int check_append(const pa::AppendArgs &a, int head_dim, int dtype, bool rope, bool fp8) {
+  if (a.num_tokens < 0 || a.num_kv_heads <= 0 || a.num_blocks <= 0 || a.num_q_heads < 0) return PA_ERR_SHAPE;
+  if (dtype != PA_FLOAT16 && dtype != PA_BFLOAT16) return PA_ERR_DTYPE;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (a.block_size != 16 && a.block_size != 32) return PA_ERR_UNSUPPORTED;
+  if (rope) {
+    if (a.rot_dim <= 0 || a.rot_dim > head_dim || a.rot_dim % 16) return PA_ERR_UNSUPPORTED;
+    if (a.max_positions <= 0) return PA_ERR_SHAPE;
+  }
+  // head counts whose rows a 32-bit index holds
+  if (a.num_q_heads > (1 << 16) || a.num_kv_heads > (1 << 16)) return PA_ERR_SHAPE;
+  if (a.num_tokens == 0) return PA_OK;
+  if (!a.k || !a.v || !a.k_cache || !a.v_cache || !a.slot_mapping) return PA_ERR_NULL;
+  if (rope && (!a.positions || !a.cos_sin || (a.num_q_heads > 0 && (!a.q || !a.q_out)))) return PA_ERR_NULL;
+  if (fp8 && (!a.k_scale || !a.v_scale)) return PA_ERR_NULL;
+  const int64_t kv_row = (int64_t)a.num_kv_heads * head_dim, q_row = (int64_t)a.num_q_heads * head_dim;
+  if (a.k_stride < kv_row || a.v_stride < kv_row) return PA_ERR_SHAPE;
+  if (a.num_q_heads > 0 && (a.q_stride < q_row || a.q_out_stride < q_row)) return PA_ERR_SHAPE;
+  if (!aligned16(a.k) || !aligned16(a.v) || !aligned16(a.k_cache) || !aligned16(a.v_cache) || a.k_stride % 8 ||
+      a.v_stride % 8 || (reinterpret_cast<uintptr_t>(a.slot_mapping) & 7u))
+    return PA_ERR_ALIGN;
+  if (rope && (!aligned16(a.cos_sin) || (reinterpret_cast<uintptr_t>(a.positions) & 7u))) return PA_ERR_ALIGN;
+  if (a.num_q_heads > 0 && (!aligned16(a.q) || !aligned16(a.q_out) || a.q_stride % 8 || a.q_out_stride % 8))
+    return PA_ERR_ALIGN;
+  if (fp8 && ((reinterpret_cast<uintptr_t>(a.k_scale) | reinterpret_cast<uintptr_t>(a.v_scale)) & 3u))
+    return PA_ERR_ALIGN;
+  return PA_OK;
+}
+
+// Tokens of one block of threads in the row part: one, so that a decode step spreads over the SMs; four once that
+// still leaves every SM several blocks (fewer, fuller blocks: 48 rows of 128 dims are 192 items for 256 threads).
+int row_tokens_per_cta(long long num_tokens, int sms) { return num_tokens >= (long long)sms * 32 ? 4 : 1; }
+
+int finish_launch(cudaError_t e) {
+  if (e != cudaSuccess) return record(e);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return record(e);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return PA_OK;
+}
+
+template <class E, int D>
+int launch_rope_write(const pa::AppendArgs &a, bool interleaved, unsigned grid, cudaStream_t stream) {
+  return finish_launch(interleaved
+                           ? launch_pdl(pa::rope_write_kv_kernel<E, D, true>, dim3(grid), dim3(256), 0, stream, a)
+                           : launch_pdl(pa::rope_write_kv_kernel<E, D, false>, dim3(grid), dim3(256), 0, stream, a));
+}
+
+template <class E, int D, int BS>
+int launch_append_fp8(const pa::AppendArgs &a, bool rope, bool interleaved, unsigned grid, cudaStream_t stream) {
+  const dim3 g(grid), b(256);
+  if (!rope) return finish_launch(launch_pdl(pa::append_fp8_kernel<E, D, BS, false, false>, g, b, 0, stream, a));
+  return finish_launch(interleaved ? launch_pdl(pa::append_fp8_kernel<E, D, BS, true, true>, g, b, 0, stream, a)
+                                   : launch_pdl(pa::append_fp8_kernel<E, D, BS, false, true>, g, b, 0, stream, a));
+}
+
+int append_fp8(pa::AppendArgs &a, int head_dim, int dtype, bool rope, bool interleaved, cudaStream_t stream) {
+  int rc = check_append(a, head_dim, dtype, rope, true);
+  if (rc != PA_OK || a.num_tokens == 0) return rc;
+  int sms = 0;
+  rc = current_sms(&sms);
+  if (rc != PA_OK) return rc;
+  // One token per warp while that keeps the warps of a few waves busy (a decode step: every token its own block);
+  // from there on block_size tokens per warp, about one run each, instead of many warps that find no run to own.
+  const long long per = 2LL * a.num_kv_heads;
+  a.tokens_per_warp = a.num_tokens * per > (long long)sms * 64 * 4 ? a.block_size : 1;
+  const long long warps = (a.num_tokens + a.tokens_per_warp - 1) / a.tokens_per_warp * per;
+  a.kv_blocks = (warps + 7) / 8;
+  a.tokens_per_cta = row_tokens_per_cta(a.num_tokens, sms);
+  const long long rows = a.num_q_heads > 0 ? (a.num_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta : 0;
+  if (a.kv_blocks + rows > 0x7fffffffLL) return PA_ERR_SHAPE;
+  const unsigned grid = (unsigned)(a.kv_blocks + rows);
+  auto go = [&](auto e) {
+    using E = decltype(e);
+    if (head_dim == 128)
+      return a.block_size == 16 ? launch_append_fp8<E, 128, 16>(a, rope, interleaved, grid, stream)
+                                : launch_append_fp8<E, 128, 32>(a, rope, interleaved, grid, stream);
+    return a.block_size == 16 ? launch_append_fp8<E, 64, 16>(a, rope, interleaved, grid, stream)
+                              : launch_append_fp8<E, 64, 32>(a, rope, interleaved, grid, stream);
+  };
+  return dtype == PA_BFLOAT16 ? go(pa::BF16{}) : go(pa::F16{});
+}
+
 }  // namespace
 
 extern "C" {
+
+int pa_rope_write_kv(const void *q, const void *k, const void *v, void *q_out, void *k_cache, void *v_cache,
+                     const int64_t *slot_mapping, const int64_t *positions, const float *cos_sin, int64_t num_tokens,
+                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim,
+                     int32_t interleaved, int32_t block_size, int64_t num_blocks, int64_t max_positions,
+                     int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                     int64_t q_out_token_stride, int32_t dtype, void *stream) {
+  pa::AppendArgs a{};
+  a.q = static_cast<const uint16_t *>(q);
+  a.k = static_cast<const uint16_t *>(k);
+  a.v = static_cast<const uint16_t *>(v);
+  a.q_out = static_cast<uint16_t *>(q_out);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.num_tokens = num_tokens;
+  a.num_blocks = num_blocks;
+  a.max_positions = max_positions;
+  a.q_stride = q_token_stride;
+  a.k_stride = k_token_stride;
+  a.v_stride = v_token_stride;
+  a.q_out_stride = q_out_token_stride;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.rot_dim = rot_dim;
+  int rc = check_append(a, head_dim, dtype, true, false);
+  if (rc != PA_OK || num_tokens == 0) return rc;
+  int sms = 0;
+  rc = current_sms(&sms);
+  if (rc != PA_OK) return rc;
+  a.tokens_per_cta = row_tokens_per_cta(num_tokens, sms);
+  const long long grid = (num_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta;
+  if (grid > 0x7fffffffLL) return PA_ERR_SHAPE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool il = interleaved != 0;
+  if (dtype == PA_BFLOAT16)
+    return head_dim == 128 ? launch_rope_write<pa::BF16, 128>(a, il, (unsigned)grid, st)
+                           : launch_rope_write<pa::BF16, 64>(a, il, (unsigned)grid, st);
+  return head_dim == 128 ? launch_rope_write<pa::F16, 128>(a, il, (unsigned)grid, st)
+                         : launch_rope_write<pa::F16, 64>(a, il, (unsigned)grid, st);
+}
+
+int pa_write_kv_fp8(const void *k, const void *v, void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                    const int64_t *slot_mapping, int64_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                    int32_t block_size, int64_t num_blocks, int64_t k_token_stride, int64_t v_token_stride,
+                    int32_t dtype, void *stream) {
+  pa::AppendArgs a{};
+  a.k = static_cast<const uint16_t *>(k);
+  a.v = static_cast<const uint16_t *>(v);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.slot_mapping = slot_mapping;
+  a.num_tokens = num_tokens;
+  a.num_blocks = num_blocks;
+  a.k_stride = k_token_stride;
+  a.v_stride = v_token_stride;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  return append_fp8(a, head_dim, dtype, false, false, static_cast<cudaStream_t>(stream));
+}
+
+int pa_rope_write_kv_fp8(const void *q, const void *k, const void *v, void *q_out, void *k_cache, void *v_cache,
+                         float *k_scale, float *v_scale, const int64_t *slot_mapping, const int64_t *positions,
+                         const float *cos_sin, int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t rot_dim, int32_t interleaved, int32_t block_size,
+                         int64_t num_blocks, int64_t max_positions, int64_t q_token_stride, int64_t k_token_stride,
+                         int64_t v_token_stride, int64_t q_out_token_stride, int32_t dtype, void *stream) {
+  pa::AppendArgs a{};
+  a.q = static_cast<const uint16_t *>(q);
+  a.k = static_cast<const uint16_t *>(k);
+  a.v = static_cast<const uint16_t *>(v);
+  a.q_out = static_cast<uint16_t *>(q_out);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.num_tokens = num_tokens;
+  a.num_blocks = num_blocks;
+  a.max_positions = max_positions;
+  a.q_stride = q_token_stride;
+  a.k_stride = k_token_stride;
+  a.v_stride = v_token_stride;
+  a.q_out_stride = q_out_token_stride;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.rot_dim = rot_dim;
+  return append_fp8(a, head_dim, dtype, true, interleaved != 0, static_cast<cudaStream_t>(stream));
+}
 
 int pa_write_kv(const void *k, const void *v, void *k_cache, void *v_cache, const int64_t *slot_mapping,
                 int64_t num_tokens, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int64_t num_blocks,

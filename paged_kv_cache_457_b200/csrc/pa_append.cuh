@@ -1,0 +1,442 @@
+// Appending a step's keys and values to the paged cache with the position
+// rotation applied on the way, into 16-bit caches and into caches held in 8
+// bits (e4m3) with one scale for each (block, kv head).
+//
+// Rotation of a row x of token t, position p = positions[t], over its first
+// r = rot_dim dims; pairs (x_i, x_{i + r/2}) (halves) or (x_{2i}, x_{2i+1})
+// (interleaved), i < r / 2, with c = cos_sin[p][i], s = cos_sin[p][r/2 + i]:
+//   x_a' = x_a c - x_b s,   x_b' = x_b c + x_a s,
+// in fp32, products and sums rounded separately (no contraction, so the
+// result is the one that elementary fp32 operations give, bit for bit).
+//
+// rope_write_kv_kernel      16-bit caches: q' out, k' and v to their slots.
+// append_fp8_kernel         8-bit caches: k' and v quantised to their slots,
+//                           q' out in the same launch (later blocks).
+//
+// A unit of work of a row is 16 elements: two 16-byte chunks that hold both
+// members of 8 pairs, with their 8 cosines and 8 sines.
+#pragma once
+
+#include <cstdint>
+
+#include "pa_kernels.cuh"
+
+namespace pa {
+
+struct AppendArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t *q_out;
+  void *k_cache, *v_cache;    // 2-byte elements, or e4m3 bytes
+  float *k_scale, *v_scale;   // [num_blocks][num_kv_heads], 8-bit caches only
+  const int64_t *slot_mapping, *positions;
+  const float *cos_sin;       // [max_positions][rot_dim]: cosines, then sines
+  long long num_tokens, num_blocks, max_positions;
+  long long q_stride, k_stride, v_stride, q_out_stride;
+  long long kv_blocks;        // append_fp8_kernel: grid blocks of the K/V part
+  int num_q_heads, num_kv_heads, block_size, rot_dim;
+  int tokens_per_cta;         // row part: consecutive tokens of one block of threads
+  int tokens_per_warp;        // append_fp8_kernel: consecutive tokens of one warp (1 or block_size)
+};
+
+// ---------------------------------------------------------------- e4m3
+// Two fp32 values to packed e4m3 (lo in the low byte), nearest even, saturating at +-448; NaN stays NaN.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Two packed e4m3 values to packed fp16 (exact: e4m3's values are fp16 values).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t x) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(x));
+  return d;
+}
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t x) {
+  const uint32_t h = e4m3x2_to_f16x2(x);
+  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// The smallest power of two s in [2^-64, 2^120] with amax <= 448 s (amax finite, >= 0).  448 = 1.75 * 2^8:
+// with amax = m 2^x, s = 2^(x - 8) while m <= 1.75, else 2^(x - 7).  Powers of two because scaling by one is
+// exact: x / s has x's bits, so a value is rounded once, to e4m3, and bytes re-scaled when a later row of the
+// block needs a larger s keep their bits unless they leave e4m3's normal range.  The price is at most one bit of
+// e4m3's 17-binade range, none of its precision.
+__device__ __forceinline__ float pow2_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = max(e, -64);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// ---------------------------------------------------------------- rotation
+// The 16-byte chunks (8 elements each) of unit c of a row, and whether the unit is rotated.
+struct Unit {
+  int c0, c1;
+  bool rotated;
+};
+template <bool INTERLEAVED>
+__device__ __forceinline__ Unit unit_of(int c, int rot_dim) {
+  const int ru = rot_dim / 16;
+  if (INTERLEAVED) return Unit{2 * c, 2 * c + 1, c < ru};
+  return c < ru ? Unit{c, c + ru, true} : Unit{2 * c, 2 * c + 1, false};
+}
+
+struct Angles {
+  float c[8], s[8];
+};
+// Cosines and sines of a rotated unit c at position p (rows of rot_dim floats, rot_dim a multiple of 16).
+__device__ __forceinline__ Angles load_angles(const AppendArgs &a, long long p, int c) {
+  Angles g;
+  const float4 *cs = reinterpret_cast<const float4 *>(a.cos_sin + p * a.rot_dim + 8 * c);
+  const float4 *sn = reinterpret_cast<const float4 *>(a.cos_sin + p * a.rot_dim + a.rot_dim / 2 + 8 * c);
+  const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1), s0 = __ldg(sn), s1 = __ldg(sn + 1);
+  g.c[0] = c0.x, g.c[1] = c0.y, g.c[2] = c0.z, g.c[3] = c0.w;
+  g.c[4] = c1.x, g.c[5] = c1.y, g.c[6] = c1.z, g.c[7] = c1.w;
+  g.s[0] = s0.x, g.s[1] = s0.y, g.s[2] = s0.z, g.s[3] = s0.w;
+  g.s[4] = s1.x, g.s[5] = s1.y, g.s[6] = s1.z, g.s[7] = s1.w;
+  return g;
+}
+
+// Turns the unit's 16 elements (chunks lo and hi) in place.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn(float (&lo)[8], float (&hi)[8], const Angles &g) {
+  auto pair = [&](float &x, float &y, int i) {
+    const float xc = __fmul_rn(x, g.c[i]), ys = __fmul_rn(y, g.s[i]);
+    const float yc = __fmul_rn(y, g.c[i]), xs = __fmul_rn(x, g.s[i]);
+    x = __fsub_rn(xc, ys);
+    y = __fadd_rn(yc, xs);
+  };
+  if (INTERLEAVED) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      pair(lo[2 * i], lo[2 * i + 1], i);
+      pair(hi[2 * i], hi[2 * i + 1], 4 + i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pair(lo[i], hi[i], i);
+  }
+}
+
+// ---------------------------------------------------------------- 16-bit rows
+// One item: unit c of rows r0 and r0 + half of token t (rows: q heads, then k heads, then v heads; half =
+// ceil(rows / 2)).  Two rows of a token share the angles and keep four 16-byte loads in flight.  q_out may be q
+// itself: a thread reads the two chunks of a row that it alone writes, before it writes them.
+template <class E, int D, bool INTERLEAVED>
+__device__ __forceinline__ void append_rows(const AppendArgs &a, long long t, int r0, int half, int rows, int c) {
+  const long long pos = a.positions[t];
+  if (pos < 0) return;  // padding: nothing of the token is touched
+  const bool pos_ok = pos < a.max_positions;
+  const bool kv = rows > a.num_q_heads;  // this launch stores K and V too
+  const long long slot = kv ? a.slot_mapping[t] : -1;
+  const bool slot_ok = slot >= 0 && slot < a.num_blocks * a.block_size;
+  if (r0 == 0 && c == 0) {
+    if (!pos_ok) atomicOr(&g_status, PA_DEV_ERR_POSITION);
+    if (slot >= 0 && !slot_ok) atomicOr(&g_status, PA_DEV_ERR_SLOT);
+  }
+  const Unit u = unit_of<INTERLEAVED>(c, a.rot_dim);
+  const long long blk = slot_ok ? slot / a.block_size : 0;
+  const int row = slot_ok ? (int)(slot - blk * a.block_size) : 0;
+  uint16_t *dst[2] = {nullptr, nullptr};  // of the first chunk; the second lies `apart` elements on
+  int apart[2];
+  bool turned[2];
+  uint4 w[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = r0 + i * half;
+    const int hk = r - a.num_q_heads, hv = hk - a.num_kv_heads;
+    const uint16_t *src = nullptr;
+    turned[i] = u.rotated && hv < 0;
+    const int c0 = hv < 0 ? u.c0 : 2 * c, c1 = hv < 0 ? u.c1 : 2 * c + 1;  // a V row keeps its chunks in order
+    apart[i] = (c1 - c0) * 8;
+    if (r < rows) {
+      if (hk < 0) {
+        src = a.q + t * a.q_stride + (long long)r * D;
+        dst[i] = a.q_out + t * a.q_out_stride + (long long)r * D + c0 * 8;
+      } else if (slot_ok && pos_ok && dcheck(blk < a.num_blocks && row < a.block_size && hv < a.num_kv_heads)) {
+        const int h = hv < 0 ? hk : hv;
+        src = (hv < 0 ? a.k + t * a.k_stride : a.v + t * a.v_stride) + (long long)h * D;
+        dst[i] = static_cast<uint16_t *>(hv < 0 ? a.k_cache : a.v_cache) +
+                 ((blk * a.num_kv_heads + h) * a.block_size + row) * D + c0 * 8;
+      }
+    }
+    if (src) {
+      w[i][0] = *reinterpret_cast<const uint4 *>(src + c0 * 8);
+      w[i][1] = *reinterpret_cast<const uint4 *>(src + c1 * 8);
+    }
+  }
+  Angles g;
+  if ((turned[0] || turned[1]) && pos_ok) g = load_angles(a, pos, c);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!dst[i]) continue;
+    if (turned[i] && pos_ok) {
+      float lo[8], hi[8];
+      E::widen8(w[i][0], lo);
+      E::widen8(w[i][1], hi);
+      turn<INTERLEAVED>(lo, hi, g);
+      w[i][0] = narrow8<E>(lo);
+      w[i][1] = narrow8<E>(hi);
+    }
+    if (!pos_ok) w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);  // only q rows get here: zeros for a bad position
+    *reinterpret_cast<uint4 *>(dst[i]) = w[i][0];
+    *reinterpret_cast<uint4 *>(dst[i] + apart[i]) = w[i][1];
+  }
+}
+
+// The row part of a launch: grid block b takes tokens b * tokens_per_cta .. of the first `rows` rows.
+template <class E, int D, bool INTERLEAVED>
+__device__ __forceinline__ void append_row_block(const AppendArgs &a, long long b, int rows) {
+  constexpr int UNITS = D / 16;
+  const int half = (rows + 1) / 2;
+  const int per = half * UNITS;
+  const long long t0 = b * a.tokens_per_cta;
+  const int nt = (int)min((long long)a.tokens_per_cta, a.num_tokens - t0);
+  for (int i = threadIdx.x; i < nt * per; i += blockDim.x) {
+    const int t = i / per, rem = i - t * per;
+    append_rows<E, D, INTERLEAVED>(a, t0 + t, rem / UNITS, half, rows, rem % UNITS);
+  }
+}
+
+template <class E, int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(256) rope_write_kv_kernel(const AppendArgs a) {
+  grid_dependency_wait();  // the rows may come from the previous kernel in the stream
+  grid_launch_dependents();
+  append_row_block<E, D, INTERLEAVED>(a, blockIdx.x, a.num_q_heads + 2 * a.num_kv_heads);
+}
+
+// ---------------------------------------------------------------- 8-bit rows
+// A run is a stretch of tokens whose slots lie in one block, whatever skipped tokens stand between them; one warp
+// handles a run for one kv head of K or of V, so a block's scale has one writer and no atomics are needed.  With x'
+// the run's rows (rotated K in fp32, V as is):
+//   amax  = largest finite |x'|,
+//   s_new = pow2_scale(amax) if the run holds the block's row 0 (the block starts anew), else
+//           max(s_old, pow2_scale(amax)); where s_new > s_old the block's bytes become rn(byte * s_old / s_new),
+//   bytes = rn_sat(x' / s_new) to the run's rows.
+// Rows are read in windows of BS tokens, kept in registers (2-byte values) between the two steps; a run is one
+// window unless skipped tokens or a slot named twice stretch it, and only then are rows read twice.
+
+// Token t of the call: its block (-1: not written), row in the block and position.  `flags`: set the status bits.
+template <int BS, bool ROPE>
+__device__ __forceinline__ long long append_token(const AppendArgs &a, long long t, bool flags, int &row,
+                                                  long long &pos) {
+  row = -1;
+  pos = 0;
+  if (t < 0 || t >= a.num_tokens) return -1;
+  const long long slot = __ldg(reinterpret_cast<const long long *>(a.slot_mapping) + t);
+  if (ROPE) pos = __ldg(reinterpret_cast<const long long *>(a.positions) + t);
+  if (pos < 0) return -1;  // padding
+  const bool slot_high = slot >= a.num_blocks * BS, pos_high = ROPE && pos >= a.max_positions;
+  if (flags && slot_high) atomicOr(&g_status, PA_DEV_ERR_SLOT);
+  if (flags && pos_high) atomicOr(&g_status, PA_DEV_ERR_POSITION);
+  if (slot < 0 || slot_high || pos_high) return -1;
+  const long long b = slot / BS;
+  row = (int)(slot - b * BS);
+  return b;
+}
+
+template <class E, int D, int BS, bool INTERLEAVED, bool ROPE>
+struct RunWindow {
+  static constexpr int LPR = D / 16;    // lanes (units) of a row
+  static constexpr int RPI = 32 / LPR;  // rows of one pass of the warp
+  static constexpr int PASSES = BS / RPI;
+  uint4 w[PASSES][2];
+  int my_row;        // lane i: row of the window's token i in the block, -1: none of the run's
+  long long my_pos;
+  int grp, c;
+  bool turned;
+  Unit u;
+
+  __device__ __forceinline__ void setup(const AppendArgs &a, bool is_v, int lane) {
+    grp = lane / LPR;
+    c = lane % LPR;
+    turned = ROPE && !is_v;
+    u = turned ? unit_of<INTERLEAVED>(c, a.rot_dim) : Unit{2 * c, 2 * c + 1, false};
+  }
+  // Tokens ts .. ts + BS - 1 of the run [ts, te) of block blk.
+  __device__ __forceinline__ void load(const AppendArgs &a, const uint16_t *base, long long stride, long long ts,
+                                       long long te, long long blk, int lane) {
+    const long long b = append_token<BS, ROPE>(a, lane < BS && ts + lane < te ? ts + lane : -1, false, my_row, my_pos);
+    if (b != blk) my_row = -1;
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const int r = p * RPI + grp;
+      const bool live = __shfl_sync(FULL, my_row, r) >= 0;
+      w[p][0] = w[p][1] = make_uint4(0, 0, 0, 0);
+      if (live) {
+        const uint16_t *src = base + (ts + r) * stride;
+        w[p][0] = __ldg(reinterpret_cast<const uint4 *>(src + u.c0 * 8));
+        w[p][1] = __ldg(reinterpret_cast<const uint4 *>(src + u.c1 * 8));
+      }
+    }
+  }
+  // This lane's 16 values of pass p in fp32 (the angles come from L1 the second time).
+  __device__ __forceinline__ void values(const AppendArgs &a, int p, float (&lo)[8], float (&hi)[8]) const {
+    E::widen8(w[p][0], lo);
+    E::widen8(w[p][1], hi);
+    if (turned) {
+      const int r = p * RPI + grp;
+      const long long pos = __shfl_sync(FULL, my_pos, r);
+      const bool live = __shfl_sync(FULL, my_row, r) >= 0;
+      if (u.rotated && live) turn<INTERLEAVED>(lo, hi, load_angles(a, pos, c));
+    }
+  }
+  // Largest finite magnitude of this lane's values.
+  __device__ __forceinline__ float amax(const AppendArgs &a, unsigned live_rows) const {
+    float m = 0.f;
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      if ((live_rows >> (p * RPI)) == 0) break;
+      float lo[8], hi[8];
+      values(a, p, lo, hi);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = fabsf(lo[i]), y = fabsf(hi[i]);
+        m = fmaxf(m, x < INFINITY ? x : 0.f);
+        m = fmaxf(m, y < INFINITY ? y : 0.f);
+      }
+    }
+    return m;
+  }
+  __device__ __forceinline__ void store(const AppendArgs &a, uint8_t *slab, float s, unsigned live_rows) const {
+    // x / s: by the exact reciprocal where s is a power of two (always, unless the caller's own scale stands)
+    const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
+    const float inv = __fdiv_rn(1.f, s);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      if ((live_rows >> (p * RPI)) == 0) break;
+      float lo[8], hi[8];
+      values(a, p, lo, hi);
+      const int row = __shfl_sync(FULL, my_row, p * RPI + grp);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo[i] = pow2 ? __fmul_rn(lo[i], inv) : __fdiv_rn(lo[i], s);
+        hi[i] = pow2 ? __fmul_rn(hi[i], inv) : __fdiv_rn(hi[i], s);
+      }
+      uint2 b0, b1;
+      b0.x = to_e4m3x2(lo[0], lo[1]) | (to_e4m3x2(lo[2], lo[3]) << 16);
+      b0.y = to_e4m3x2(lo[4], lo[5]) | (to_e4m3x2(lo[6], lo[7]) << 16);
+      b1.x = to_e4m3x2(hi[0], hi[1]) | (to_e4m3x2(hi[2], hi[3]) << 16);
+      b1.y = to_e4m3x2(hi[4], hi[5]) | (to_e4m3x2(hi[6], hi[7]) << 16);
+      if (row >= 0 && dcheck(row < BS)) {
+        *reinterpret_cast<uint2 *>(slab + row * D + u.c0 * 8) = b0;
+        *reinterpret_cast<uint2 *>(slab + row * D + u.c1 * 8) = b1;
+      }
+    }
+  }
+};
+
+template <class E, int D, int BS, bool INTERLEAVED, bool ROPE>
+__device__ __forceinline__ void append_run(const AppendArgs &a, bool is_v, int h, long long ts, long long te,
+                                           long long blk, int lane) {
+  if (!dcheck(blk >= 0 && blk < a.num_blocks && h < a.num_kv_heads)) return;
+  const uint16_t *base = (is_v ? a.v : a.k) + (long long)h * D;
+  const long long stride = is_v ? a.v_stride : a.k_stride;
+  float *scale = (is_v ? a.v_scale : a.k_scale) + blk * a.num_kv_heads + h;
+  uint8_t *slab = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + (blk * a.num_kv_heads + h) * BS * D;
+  const float s_old = *scale;
+  RunWindow<E, D, BS, INTERLEAVED, ROPE> win;
+  win.setup(a, is_v, lane);
+  float amax = 0.f;
+  bool fresh = false;
+  unsigned live = 0;
+  for (long long t = ts; t < te; t += BS) {
+    win.load(a, base, stride, t, te, blk, lane);
+    live = __ballot_sync(FULL, win.my_row >= 0);
+    amax = fmaxf(amax, win.amax(a, live));
+    fresh |= __any_sync(FULL, win.my_row == 0);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, off));
+  const float want = pow2_scale(amax);
+  const float s_new = fresh ? want : fmaxf(s_old, want);
+
+  if (!fresh && s_new > s_old) {  // rows of earlier calls, in units of the larger scale
+    const float ratio = __fdiv_rn(s_old, s_new);
+    uint4 *b = reinterpret_cast<uint4 *>(slab);
+#pragma unroll
+    for (int i = 0; i < BS * D / 512; ++i) {
+      const uint4 x = b[i * 32 + lane];
+      const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+      uint32_t out[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f0 = e4m3x2_to_float2((uint16_t)in[j]), f1 = e4m3x2_to_float2((uint16_t)(in[j] >> 16));
+        out[j] = to_e4m3x2(__fmul_rn(f0.x, ratio), __fmul_rn(f0.y, ratio)) |
+                 (to_e4m3x2(__fmul_rn(f1.x, ratio), __fmul_rn(f1.y, ratio)) << 16);
+      }
+      b[i * 32 + lane] = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+    __syncwarp();  // before the run's own rows are written over theirs
+  }
+  if (te - ts <= BS) {
+    win.store(a, slab, s_new, live);
+  } else {
+    for (long long t = ts; t < te; t += BS) {
+      win.load(a, base, stride, t, te, blk, lane);
+      win.store(a, slab, s_new, __ballot_sync(FULL, win.my_row >= 0));
+      __syncwarp();
+    }
+  }
+  if (lane == 0) *scale = s_new;
+}
+
+// K/V part: warp w of the part takes tokens [i * tokens_per_warp, +tokens_per_warp) of one kv head of K or V, and
+// the runs that START among them (a run's later tokens may lie in the next warps' stretches, which then leave
+// them alone).  Row part (grid blocks from kv_blocks on): the q heads.
+template <class E, int D, int BS, bool INTERLEAVED, bool ROPE>
+__global__ void __launch_bounds__(256) append_fp8_kernel(const AppendArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (ROPE && (long long)blockIdx.x >= a.kv_blocks) {
+    append_row_block<E, D, INTERLEAVED>(a, (long long)blockIdx.x - a.kv_blocks, a.num_q_heads);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int per = 2 * a.num_kv_heads;
+  const long long t0 = (w / per) * a.tokens_per_warp;
+  if (t0 >= a.num_tokens) return;
+  const int hw = (int)(w % per);
+  const bool is_v = hw >= a.num_kv_heads;
+  const int h = is_v ? hw - a.num_kv_heads : hw;
+  int row;
+  long long pos;
+  const long long mine =
+      append_token<BS, ROPE>(a, lane < a.tokens_per_warp ? t0 + lane : -1, hw == 0, row, pos);
+  const unsigned written = __ballot_sync(FULL, mine >= 0);
+  if (!written) return;
+  // block of the last written token before this stretch (-1: none)
+  long long before = -1;
+  for (long long t = t0 - 1; t >= 0; t -= 32) {
+    const long long b = append_token<BS, ROPE>(a, t - lane, false, row, pos);
+    const unsigned m = __ballot_sync(FULL, b >= 0);
+    if (m) {
+      before = __shfl_sync(FULL, b, __ffs(m) - 1);
+      break;
+    }
+  }
+  // a written token starts a run where the written token before it lies in another block
+  const unsigned below = written & ((1u << lane) - 1u);
+  const long long prev = __shfl_sync(FULL, mine, below ? 31 - __clz(below) : 0);
+  unsigned heads = __ballot_sync(FULL, mine >= 0 && mine != (below ? prev : before));
+  while (heads) {
+    const int i = __ffs(heads) - 1;
+    heads &= heads - 1;
+    const long long blk = __shfl_sync(FULL, mine, i);
+    const long long ts = t0 + i;
+    // the run ends before the next written token of another block; `te` is one past its last token
+    long long te = ts + 1;
+    for (long long t = ts + 1; t < a.num_tokens; t += 32) {
+      const long long b = append_token<BS, ROPE>(a, t + lane, false, row, pos);
+      const unsigned other = __ballot_sync(FULL, b >= 0 && b != blk);
+      unsigned same = __ballot_sync(FULL, b == blk);
+      if (other) same &= (other & (0u - other)) - 1u;  // those before the first of another block
+      if (same) te = t + 32 - __clz(same);
+      if (other) break;
+    }
+    append_run<E, D, BS, INTERLEAVED, ROPE>(a, is_v, h, ts, te, blk, lane);
+  }
+}
+
+}  // namespace pa
