@@ -497,6 +497,28 @@ int pa_decode_cascade(const void *q, const void *k_cache, const void *v_cache, c
                       const int32_t *plan, const pa_cascade_info *info, void *workspace, size_t workspace_bytes,
                       void *stream);
 
+/*
+ * pa_decode_fp8 -- pa_decode over an 8-bit cache (see "caches held in 8
+ * bits"): K_j = value(byte) * k_scale[block][h] and V_j likewise.  Arguments
+ * and device-side errors as pa_decode; q and out are of `dtype`.  Products
+ * and sums are fp32; each softmax weight is rounded to fp16 (11 bits) before
+ * it multiplies V, and summed as rounded.  partition_tokens counts tokens per
+ * chunk, rounded up to 32.  K/V bytes of rows past a context, and entries
+ * past its last block, may hold anything.  num_blocks * num_kv_heads *
+ * block_size must not exceed 2^31 - 1 (PA_ERR_SHAPE).  Caches are 16-byte
+ * aligned, scales 4-byte.
+ * The workspace (pa_decode_fp8_workspace_size bytes, 16-byte aligned) is
+ * scratch of one call in flight at a time.
+ */
+size_t pa_decode_fp8_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                    int32_t block_size, int32_t max_context_len, int32_t partition_tokens);
+int pa_decode_fp8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
+                  const int32_t *block_tables, const int32_t *context_lens, float scale, void *out, int32_t num_seqs,
+                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                  int64_t num_blocks, int32_t block_table_stride, int32_t max_context_len, int64_t q_seq_stride,
+                  int64_t out_seq_stride, int32_t partition_tokens, int32_t dtype, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
 /* pa_version -- library ABI version (major * 10000 + minor * 100 + patch). */
 int32_t pa_version(void);
 

@@ -18,6 +18,7 @@
 #include "pa_b200.h"
 #include "pa_cascade.cuh"
 #include "pa_copy.cuh"
+#include "pa_fp8.cuh"
 #include "pa_kernels.cuh"
 #include "pa_prefill.cuh"
 #include "pa_mma.cuh"
@@ -630,9 +631,201 @@ int append_fp8(pa::AppendArgs &a, int head_dim, int dtype, bool rope, bool inter
   return dtype == PA_BFLOAT16 ? go(pa::BF16{}) : go(pa::F16{});
 }
 
+// ---- decode over 8-bit caches (pa_fp8.cuh)
+
+// Launch shape of the 8-bit split kernel; overridable at build time for tuning sweeps.
+#ifndef PA_WARPS8
+#define PA_WARPS8 4
+#endif
+#ifndef PA_STAGES8
+#define PA_STAGES8 2
+#endif
+#ifndef PA_BLOCKS8
+#define PA_BLOCKS8 3
+#endif
+#ifndef PA_TAIL_CHUNKS8
+#define PA_TAIL_CHUNKS8 1
+#endif
+constexpr int kWarps8 = PA_WARPS8, kStages8 = PA_STAGES8, kBlocks8 = PA_BLOCKS8;
+static_assert(kWarps8 == kWarps, "blocks_per_sm sizes blocks with kWarps warps");
+
+// Query heads handled together: the largest divisor of the group not above 8 (the mma's columns); one kernel serves
+// every group size, since the products per byte do not bound it.
+int heads_per_unit8(int group) {
+  for (int c = 8; c > 1; --c)
+    if (group % c == 0) return c;
+  return 1;
+}
+
+template <class E, int D>
+const void *split8_kernel() {
+  return reinterpret_cast<const void *>(pa::decode8_split_kernel<E, D, kWarps8, kStages8, kBlocks8>);
+}
+const void *split8_kernel_for(int dtype, int head_dim) {
+  if (dtype == PA_BFLOAT16) return head_dim == 128 ? split8_kernel<pa::BF16, 128>() : split8_kernel<pa::BF16, 64>();
+  return head_dim == 128 ? split8_kernel<pa::F16, 128>() : split8_kernel<pa::F16, 64>();
+}
+uint32_t split8_smem(int head_dim, int num_seqs) {
+  return head_dim == 128 ? pa::Smem8<128, kWarps8, kStages8>::bytes(num_seqs)
+                         : pa::Smem8<64, kWarps8, kStages8>::bytes(num_seqs);
+}
+
+// As plan_decode, on tiles of pa::TILE8 tokens.
+int plan_decode8(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len,
+                 int partition_tokens, int dtype, LaunchPlan *lp) {
+  if (partition_tokens < 0 || partition_tokens % pa::TILE != 0) return PA_ERR_PARTITION;
+  int sms = 0;
+  int rc = current_sms(&sms);
+  if (rc != PA_OK) return rc;
+  const int group = num_q_heads / num_kv_heads;
+  const int G = heads_per_unit8(group);
+  lp->segment_mode = false;
+  lp->smem = split8_smem(head_dim, num_seqs);
+  if (lp->smem > 227u * 1024u) return PA_ERR_SHAPE;
+  int occ_f16 = 0, occ_bf16 = 0;
+  if ((rc = blocks_per_sm(split8_kernel_for(PA_FLOAT16, head_dim), lp->smem, &occ_f16)) != PA_OK) return rc;
+  if ((rc = blocks_per_sm(split8_kernel_for(PA_BFLOAT16, head_dim), lp->smem, &occ_bf16)) != PA_OK) return rc;
+  const long long ws_warps = (long long)sms * std::max(occ_f16, occ_bf16) * kWarps8;
+  lp->grid = dtype == 0 ? 0 : sms * (dtype == PA_BFLOAT16 ? occ_bf16 : occ_f16);
+  lp->chunk_tiles = (partition_tokens + pa::TILE8 - 1) / pa::TILE8;
+  if (lp->chunk_tiles == 0) {
+    lp->max_chunks = ws_warps * (1 + PA_TAIL_CHUNKS8) + 1;
+  } else {
+    const long long per_seq = ((long long)max_context_len + pa::TILE8 - 1) / pa::TILE8;
+    const long long total = (long long)num_seqs * num_kv_heads * (group / G) * per_seq;
+    lp->max_chunks = std::max(1LL, (total + lp->chunk_tiles - 1) / lp->chunk_tiles);
+  }
+  lp->queue_bytes = 256;
+  lp->tiles_bytes = (((size_t)num_seqs + 1) * sizeof(int) + 255) / 256 * 256;
+  lp->ml_bytes = (size_t)lp->max_chunks * 2 * G * sizeof(float2);
+  lp->ml_bytes = (lp->ml_bytes + 255) / 256 * 256;
+  lp->acc_bytes = (size_t)lp->max_chunks * 2 * G * head_dim * sizeof(float);
+  lp->total_bytes = lp->queue_bytes + lp->tiles_bytes + lp->ml_bytes + lp->acc_bytes;
+  return PA_OK;
+}
+
+// 2-D map of an 8-bit cache, [num_blocks * num_kv_heads * block_size rows][head_dim bytes], boxes of one
+// (block, head) slab, swizzled over the row's 64 or 128 bytes.
+int fp8_tensor_map(const void *base, long long rows, int head_dim, int block_size, CUtensorMap *out) {
+  int rc = PA_OK;
+  auto encode = tensor_map_encoder(&rc);
+  if (!encode) return rc;
+  const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)head_dim};
+  const cuuint32_t box[2] = {(cuuint32_t)head_dim, (cuuint32_t)block_size};
+  const cuuint32_t elem_strides[2] = {1, 1};
+  const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+                            elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    t_last_cuda_error = "cuTensorMapEncodeTiled failed for an 8-bit cache (code " + std::to_string((int)r) + ")";
+    return PA_ERR_CUDA;
+  }
+  return PA_OK;
+}
+
+template <class E, int D>
+int launch_decode8(const pa::Decode8Args &a, const LaunchPlan &lp, const CUtensorMap &mk, const CUtensorMap &mv,
+                   cudaStream_t stream) {
+  int rc = finish_launch(launch_pdl(pa::decode8_split_kernel<E, D, kWarps8, kStages8, kBlocks8>, dim3(lp.grid),
+                                    dim3(kWarps8 * 32), lp.smem, stream, mk, mv, a));
+  if (rc != PA_OK) return rc;
+  // one warp per two heads of a segment (one for an odd number of heads), as after decode_split_mma_kernel
+  const int hw = a.d.heads_per_unit % 2 == 0 ? 2 : 1;
+  const long long warps = (long long)a.d.num_seqs * a.d.num_kv_heads * a.d.n_chunks * (a.d.heads_per_unit / hw);
+  const dim3 grid((unsigned)((warps + 7) / 8)), block(256);
+  return finish_launch(hw == 2 ? launch_pdl(pa::decode_merge_kernel<E, D, 2, 4>, grid, block, 0, stream, a.d)
+                               : launch_pdl(pa::decode_merge_kernel<E, D, 1, 4>, grid, block, 0, stream, a.d));
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t pa_decode_fp8_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                    int32_t block_size, int32_t max_context_len, int32_t partition_tokens) {
+  if (check_decode_shape(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len) != PA_OK)
+    return 0;
+  LaunchPlan lp;
+  if (plan_decode8(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, partition_tokens, 0, &lp) != PA_OK)
+    return 0;
+  return lp.total_bytes;
+}
+
+int pa_decode_fp8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
+                  const int32_t *block_tables, const int32_t *context_lens, float scale, void *out, int32_t num_seqs,
+                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                  int64_t num_blocks, int32_t block_table_stride, int32_t max_context_len, int64_t q_seq_stride,
+                  int64_t out_seq_stride, int32_t partition_tokens, int32_t dtype, void *workspace,
+                  size_t workspace_bytes, void *stream) {
+  int rc = check_decode_shape(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len);
+  if (rc != PA_OK) return rc;
+  if (dtype != PA_FLOAT16 && dtype != PA_BFLOAT16) return PA_ERR_DTYPE;
+  if (num_blocks <= 0 || block_table_stride <= 0) return PA_ERR_SHAPE;
+  const int64_t row = (int64_t)num_q_heads * head_dim;
+  if (q_seq_stride < row || out_seq_stride < row) return PA_ERR_SHAPE;
+  if (partition_tokens < 0 || partition_tokens % pa::TILE != 0) return PA_ERR_PARTITION;
+  if (!std::isfinite(scale)) return PA_ERR_SHAPE;
+  if (num_blocks > 0x7fffffffLL / ((long long)num_kv_heads * block_size)) return PA_ERR_SHAPE;  // TMA coordinates
+  if (num_seqs == 0) return PA_OK;
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables || !context_lens || !out) return PA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || (q_seq_stride % 8) ||
+      (out_seq_stride % 8))
+    return PA_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale) |
+       reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens)) & 3u)
+    return PA_ERR_ALIGN;
+  LaunchPlan lp;
+  rc = plan_decode8(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, partition_tokens, dtype, &lp);
+  if (rc != PA_OK) return rc;
+  if (!workspace || workspace_bytes < lp.total_bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+  CUtensorMap mk, mv;
+  const long long rows = num_blocks * num_kv_heads * block_size;
+  if ((rc = fp8_tensor_map(k_cache, rows, head_dim, block_size, &mk)) != PA_OK) return rc;
+  if ((rc = fp8_tensor_map(v_cache, rows, head_dim, block_size, &mv)) != PA_OK) return rc;
+
+  const int group = num_q_heads / num_kv_heads;
+  char *ws = static_cast<char *>(workspace);
+  pa::Decode8Args args{};
+  pa::DecodeArgs &a = args.d;
+  a.q = static_cast<const uint16_t *>(q);
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.out = static_cast<uint16_t *>(out);
+  a.ws_queue = reinterpret_cast<unsigned long long *>(ws);
+  a.ws_tiles = reinterpret_cast<int *>(ws + lp.queue_bytes);
+  a.ws_ml = reinterpret_cast<float2 *>(ws + lp.queue_bytes + lp.tiles_bytes);
+  a.ws_acc = reinterpret_cast<float *>(ws + lp.queue_bytes + lp.tiles_bytes + lp.ml_bytes);
+  a.num_blocks = num_blocks;
+  a.q_seq_stride = q_seq_stride;
+  a.out_seq_stride = out_seq_stride;
+  a.max_chunks = lp.max_chunks;
+  a.wait_limit_ns = kWaitLimitNs;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);  // log2(e)
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.table_stride = block_table_stride;
+  a.max_context_len = max_context_len;
+  a.group = group;
+  a.heads_per_unit = heads_per_unit8(group);
+  a.n_chunks = group / a.heads_per_unit;
+  a.chunk_tiles = lp.chunk_tiles;
+  a.split_warps = lp.grid * kWarps8;
+  a.static_permille = 0;
+  a.tail_chunks_per_warp = PA_TAIL_CHUNKS8;
+  a.epoch = next_epoch();
+  args.k_scale = k_scale;
+  args.v_scale = v_scale;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == PA_BFLOAT16)
+    return head_dim == 128 ? launch_decode8<pa::BF16, 128>(args, lp, mk, mv, st)
+                           : launch_decode8<pa::BF16, 64>(args, lp, mk, mv, st);
+  return head_dim == 128 ? launch_decode8<pa::F16, 128>(args, lp, mk, mv, st)
+                         : launch_decode8<pa::F16, 64>(args, lp, mk, mv, st);
+}
 
 int pa_rope_write_kv(const void *q, const void *k, const void *v, void *q_out, void *k_cache, void *v_cache,
                      const int64_t *slot_mapping, const int64_t *positions, const float *cos_sin, int64_t num_tokens,

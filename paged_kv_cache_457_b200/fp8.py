@@ -1,0 +1,96 @@
+"""Attention over paged caches held in 8 bits (e4m3) with one scale for each block and kv head.
+
+Argument marshalling only; caches and scales as :mod:`.append` describes and fills them.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from .append import fp8_geometry, on_device, token_stride
+
+
+def bind(lib: ctypes.CDLL) -> None:
+    vp, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    sig = {
+        "pa_decode_fp8_workspace_size": (sz, [i32] * 7),
+        "pa_decode_fp8": (ctypes.c_int, [vp] * 7 + [f32, vp] + [i32] * 5 + [i64, i32, i32, i64, i64, i32, i32, vp, sz,
+                                                                            vp]),
+    }
+    for name, (res, args) in sig.items():
+        f = getattr(lib, name)
+        f.restype = res
+        f.argtypes = args
+
+
+def _tables(block_tables: torch.Tensor, context_lens: torch.Tensor, S: int) -> int:
+    """Checks the batch's tables and lengths; returns the table's row stride."""
+    from . import PagedAttentionError
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != S \
+            or (block_tables.shape[1] > 1 and block_tables.stride(1) != 1):
+        raise PagedAttentionError("block_tables must be int32 [S, max_blocks] with contiguous rows")
+    if context_lens.dtype != torch.int32 or tuple(context_lens.shape) != (S,) or not context_lens.is_contiguous():
+        raise PagedAttentionError("context_lens must be a contiguous int32 [S] tensor")
+    # a single row's stride says nothing: its width is the capacity
+    return block_tables.stride(0) if S > 1 else block_tables.shape[1]
+
+
+def _scratch(dev: torch.device, stream: int, nbytes: int) -> torch.Tensor | None:
+    """Workspace of a call: kept per device and stream, but a capture gets its own from the graph's pool, since a
+    captured graph may be replayed beside other calls and must not share (or outlive) theirs."""
+    from . import _workspace
+    if nbytes and torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return _workspace(dev, stream, nbytes)
+
+
+def decode_fp8_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                              partition_tokens: int = 0) -> int:
+    """Device workspace bytes of :func:`decode_fp8` for these sizes on the current device (0 on bad input)."""
+    from . import load_library
+    return int(load_library().pa_decode_fp8_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                           max_context_len, partition_tokens))
+
+
+def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+               v_scale: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+               max_context_len: int | None = None, out: torch.Tensor | None = None, partition_tokens: int = 0,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """:func:`decode` over an 8-bit cache: attention of q ([S, Hq, d], float16 or bfloat16) over each sequence's
+    context; returns out ([S, Hq, d], q's dtype).  Other arguments as :func:`decode`."""
+    from . import PagedAttentionError, _DTYPES, _check, _need_cuda, _stream, load_library
+    dev = k_cache.device
+    for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
+                    ("block_tables", block_tables), ("context_lens", context_lens)):
+        _need_cuda(name, t, dev)
+    nb, hkv, bs, d = fp8_geometry(k_cache, v_cache, k_scale, v_scale)
+    if q.dtype not in _DTYPES or q.dim() != 3:
+        raise PagedAttentionError("q must be float16 or bfloat16 [S, Hq, d]")
+    S, hq = q.shape[0], q.shape[1]
+    qs = token_stride("q", q, (S, hq, d), q.dtype)
+    ts = _tables(block_tables, context_lens, S)
+    if out is None:
+        out = torch.empty((S, hq, d), dtype=q.dtype, device=dev)
+        os_ = hq * d
+    else:
+        _need_cuda("out", out, dev)
+        os_ = token_stride("out", out, (S, hq, d), q.dtype)
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if S else 0
+    lib = load_library()
+    with on_device(dev):
+        stream = _stream(dev)
+        if workspace is None:
+            workspace = _scratch(dev, stream, int(lib.pa_decode_fp8_workspace_size(
+                S, hq, hkv, d, bs, int(max_context_len), int(partition_tokens))))
+        elif not (workspace.is_cuda and workspace.device == dev and workspace.is_contiguous()):
+            raise PagedAttentionError("workspace must be a contiguous tensor on the caches' device")
+        rc = lib.pa_decode_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                               v_scale.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), float(scale),
+                               out.data_ptr(), S, hq, hkv, d, bs, nb, ts if S else 1, int(max_context_len), qs, os_,
+                               int(partition_tokens), _DTYPES[q.dtype],
+                               workspace.data_ptr() if workspace is not None else None,
+                               workspace.numel() * workspace.element_size() if workspace is not None else 0, stream)
+    _check(rc, "pa_decode_fp8")
+    return out

@@ -96,13 +96,14 @@ def values(cache: np.ndarray, scale: np.ndarray) -> np.ndarray:
     return E4M3[cache] * scale.astype(np.float64)[:, :, None, None]
 
 
-def attention(q, k_pool, v_pool, tables, ctx, scale, new=None):
+def attention(q, k_pool, v_pool, tables, ctx, scale, new=None, bounds=False):
     """Attention in float64 of q [N, Hq, d] over pools [NB, H, bs, d] (float64): sequence s brings its last new[s]
-    (default 1) tokens, causal.  Sequences without context give zeros."""
+    (default 1) tokens, causal.  Sequences without context give zeros.  With ``bounds`` also, per output element,
+    sum_j w_j |v_j|, and per (token, head) the largest sum_i |scale q_i k_ji| over its keys."""
     q = np.asarray(q, np.float64)
     hkv, bs, d = k_pool.shape[1:]
     group = q.shape[1] // hkv
-    out = np.zeros_like(q)
+    out, mean_abs, dots = np.zeros_like(q), np.zeros_like(q), np.zeros(q.shape[:2])
     new = np.ones(len(ctx), int) if new is None else np.asarray(new)
     at = 0
     for s, L in enumerate(ctx):
@@ -112,12 +113,17 @@ def attention(q, k_pool, v_pool, tables, ctx, scale, new=None):
             ids = tables[s, :-(-L // bs)]
             k = k_pool[ids].transpose(1, 0, 2, 3).reshape(hkv, -1, d)[:, :L]
             v = v_pool[ids].transpose(1, 0, 2, 3).reshape(hkv, -1, d)[:, :L]
+            seen = np.arange(L)[None, None] <= np.arange(L - n, L)[None, :, None]
             for h in range(hkv):
-                qh = q[at:at + n, h * group:(h + 1) * group].transpose(1, 0, 2)
-                z = np.einsum("gtd,jd->gtj", qh, k[h]) * scale
-                z = np.where(np.arange(L)[None, None] <= np.arange(L - n, L)[None, :, None], z, -np.inf)
+                heads = slice(h * group, (h + 1) * group)
+                qh = q[at:at + n, heads].transpose(1, 0, 2)
+                z = np.where(seen, np.matmul(qh, k[h].T) * scale, -np.inf)
                 w = np.exp(z - z.max(-1, keepdims=True))
-                o = np.einsum("gtj,jd->gtd", w / w.sum(-1, keepdims=True), v[h])
-                out[at:at + n, h * group:(h + 1) * group] = o.transpose(1, 0, 2)
+                w /= w.sum(-1, keepdims=True)
+                out[at:at + n, heads] = np.matmul(w, v[h]).transpose(1, 0, 2)
+                if bounds:
+                    mean_abs[at:at + n, heads] = np.matmul(w, np.abs(v[h])).transpose(1, 0, 2)
+                    b = np.where(seen, np.matmul(np.abs(qh), np.abs(k[h]).T) * abs(scale), 0.0)
+                    dots[at:at + n, heads] = b.max(-1).T
         at += n
-    return out
+    return (out, mean_abs, dots) if bounds else out
