@@ -519,6 +519,31 @@ int pa_decode_fp8(const void *q, const void *k_cache, const void *v_cache, const
                   int64_t out_seq_stride, int32_t partition_tokens, int32_t dtype, void *workspace,
                   size_t workspace_bytes, void *stream);
 
+/*
+ * pa_prefill_fp8 -- pa_prefill over an 8-bit cache whose rows of the new
+ * tokens are already written (pa_write_kv_fp8, pa_rope_write_kv_fp8).
+ * Arguments, layouts and device-side errors as pa_prefill, except that a
+ * needed table entry outside the pool zeroes the (256 new tokens, head) items
+ * that need it.  K and V are widened and scaled to the storage type of q
+ * (exact where the scale is a power of two and the value a normal number of
+ * that type, saturating at fp16's largest value otherwise), products and sums
+ * are fp32, softmax weights are rounded to the storage type.  Any finite
+ * `scale`.  A NaN among the values of a sequence's live tokens may reach all
+ * of its rows in the call.
+ *   workspace   device scratch of pa_prefill_fp8_workspace_size bytes,
+ *               16-byte aligned; needs no initialisation.  Calls that may run
+ *               at the same time must not share one.
+ */
+size_t pa_prefill_fp8_workspace_size(int32_t num_seqs, int64_t num_query_tokens, int32_t num_q_heads,
+                                     int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                     int32_t max_query_len);
+int pa_prefill_fp8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                   const float *v_scale, const int32_t *block_tables, const int32_t *query_start,
+                   const int32_t *context_lens, float scale, void *out, int32_t num_seqs, int64_t num_query_tokens,
+                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                   int64_t num_blocks, int32_t block_table_stride, int32_t max_query_len, int64_t q_token_stride,
+                   int64_t out_token_stride, int32_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
 /* pa_version -- library ABI version (major * 10000 + minor * 100 + patch). */
 int32_t pa_version(void);
 

@@ -21,6 +21,7 @@
 #include "pa_fp8.cuh"
 #include "pa_kernels.cuh"
 #include "pa_prefill.cuh"
+#include "pa_prefill8.cuh"
 #include "pa_mma.cuh"
 #include "pa_stream.cuh"
 
@@ -739,6 +740,17 @@ int launch_decode8(const pa::Decode8Args &a, const LaunchPlan &lp, const CUtenso
                                : launch_pdl(pa::decode_merge_kernel<E, D, 1, 4>, grid, block, 0, stream, a.d));
 }
 
+int check_prefill8_shape(int32_t num_seqs, int64_t num_query_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t block_size, int32_t max_query_len) {
+  if (num_seqs < 0 || num_query_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_query_len < 0)
+    return PA_ERR_SHAPE;
+  if (num_seqs > 65535 || num_q_heads > 65535 || num_query_tokens > 0x7fffffffLL) return PA_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
+  if (num_q_heads % num_kv_heads != 0) return PA_ERR_HEADS;
+  return PA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1347,6 +1359,104 @@ int pa_prefill(const void *q, const void *k_cache, const void *v_cache, const in
   }
   if (head_dim == 128) return launch(pa::prefill_tc_kernel<pa::F16, 128>, pa::PrefillSmem<128>::ALLOC);
   return launch(pa::prefill_tc_kernel<pa::F16, 64>, pa::PrefillSmem<64>::ALLOC);
+}
+
+size_t pa_prefill_fp8_workspace_size(int32_t num_seqs, int64_t num_query_tokens, int32_t num_q_heads,
+                                     int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                     int32_t max_query_len) {
+  if (check_prefill8_shape(num_seqs, num_query_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                           max_query_len) != PA_OK)
+    return 0;
+  return 256;  // the work counter
+}
+
+int pa_prefill_fp8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                   const float *v_scale, const int32_t *block_tables, const int32_t *query_start,
+                   const int32_t *context_lens, float scale, void *out, int32_t num_seqs, int64_t num_query_tokens,
+                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                   int64_t num_blocks, int32_t block_table_stride, int32_t max_query_len, int64_t q_token_stride,
+                   int64_t out_token_stride, int32_t dtype, void *workspace, size_t workspace_bytes, void *stream) {
+  int rc = check_prefill8_shape(num_seqs, num_query_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                                max_query_len);
+  if (rc != PA_OK) return rc;
+  if (num_blocks < 0 || block_table_stride < 0) return PA_ERR_SHAPE;
+  if (dtype != PA_FLOAT16 && dtype != PA_BFLOAT16) return PA_ERR_DTYPE;
+  if (!std::isfinite(scale)) return PA_ERR_SHAPE;
+  if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return PA_OK;
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables || !query_start || !context_lens || !out)
+    return PA_ERR_NULL;
+  const long long qrow = (long long)num_q_heads * head_dim;
+  if (q_token_stride < qrow || out_token_stride < qrow) return PA_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || (q_token_stride % 8) ||
+      (out_token_stride % 8))
+    return PA_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale) |
+       reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(query_start) |
+       reinterpret_cast<uintptr_t>(context_lens)) & 3u)
+    return PA_ERR_ALIGN;
+  if (num_blocks == 0) return PA_ERR_SHAPE;
+  if (!workspace || workspace_bytes < 256 || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+  auto encode = tensor_map_encoder(&rc);
+  if (!encode) return rc;
+  CUtensorMap mq;
+  {
+    // q viewed as [tokens][heads][head_dim]; one box = 128 tokens x 64 dims of one head
+    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)num_q_heads, (cuuint64_t)num_query_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)q_token_stride * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)pa::PF_BM};
+    const cuuint32_t elem_strides[3] = {1, 1, 1};
+    const CUresult r =
+        encode(&mq, dtype == PA_BFLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+               const_cast<void *>(q), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+      t_last_cuda_error = "cuTensorMapEncodeTiled failed for q (code " + std::to_string((int)r) + ")";
+      return PA_ERR_CUDA;
+    }
+  }
+  pa::Prefill8Args args{};
+  pa::PrefillArgs &a = args.p;
+  a.block_tables = block_tables;
+  a.query_start = query_start;
+  a.context_lens = context_lens;
+  a.out = static_cast<uint16_t *>(out);
+  a.num_blocks = num_blocks;
+  a.out_token_stride = out_token_stride;
+  a.num_query_tokens = num_query_tokens;
+  a.wait_limit_ns = kWaitLimitNs;
+  args.k_sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
+  a.scale_log2 = scale == 0.f ? 1.f : (float)(std::fabs((double)scale) * 1.4426950408889634);  // log2(e)
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.table_stride = block_table_stride;
+  a.q_tiles = (int)(((long long)max_query_len + pa::PF_ROWS - 1) / pa::PF_ROWS);
+  a.num_items = (long long)a.q_tiles * num_q_heads * num_seqs;
+  a.queue = static_cast<unsigned int *>(workspace);
+  args.k_cache = static_cast<const uint8_t *>(k_cache);
+  args.v_cache = static_cast<const uint8_t *>(v_cache);
+  args.k_scale = k_scale;
+  args.v_scale = v_scale;
+  if (a.num_items > 0x7fffffffLL) return PA_ERR_SHAPE;  // the 32-bit counter, with room for the last takers
+  int sms = 0;
+  rc = current_sms(&sms);
+  if (rc != PA_OK) return rc;
+  const dim3 grid((unsigned)std::min<long long>(a.num_items, sms));  // persistent: one CTA fills an SM
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t me = cudaMemsetAsync(a.queue, 0, sizeof(unsigned int), st);
+  if (me != cudaSuccess) return record(me);
+  auto launch = [&](auto kernel, uint32_t smem) -> int {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return record(e);
+    return finish_launch(launch_pdl(kernel, grid, dim3(pa::PF8_THREADS), smem, st, mq, args));
+  };
+  if (dtype == PA_BFLOAT16) {
+    if (head_dim == 128) return launch(pa::prefill8_tc_kernel<pa::BF16, 128>, pa::PrefillSmem<128>::ALLOC);
+    return launch(pa::prefill8_tc_kernel<pa::BF16, 64>, pa::PrefillSmem<64>::ALLOC);
+  }
+  if (head_dim == 128) return launch(pa::prefill8_tc_kernel<pa::F16, 128>, pa::PrefillSmem<128>::ALLOC);
+  return launch(pa::prefill8_tc_kernel<pa::F16, 64>, pa::PrefillSmem<64>::ALLOC);
 }
 
 int pa_read_bandwidth_probe(const void *src, int64_t bytes, uint32_t *sink, void *stream) {

@@ -17,6 +17,9 @@ def bind(lib: ctypes.CDLL) -> None:
         "pa_decode_fp8_workspace_size": (sz, [i32] * 7),
         "pa_decode_fp8": (ctypes.c_int, [vp] * 7 + [f32, vp] + [i32] * 5 + [i64, i32, i32, i64, i64, i32, i32, vp, sz,
                                                                             vp]),
+        "pa_prefill_fp8_workspace_size": (sz, [i32, i64, i32, i32, i32, i32, i32]),
+        "pa_prefill_fp8": (ctypes.c_int, [vp] * 8 + [f32, vp, i32, i64] + [i32] * 4 + [i64, i32, i32, i64, i64, i32, vp,
+                                                                                     sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -93,4 +96,48 @@ def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
                                workspace.data_ptr() if workspace is not None else None,
                                workspace.numel() * workspace.element_size() if workspace is not None else 0, stream)
     _check(rc, "pa_decode_fp8")
+    return out
+
+
+def prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                v_scale: torch.Tensor, block_tables: torch.Tensor, query_start: torch.Tensor,
+                context_lens: torch.Tensor, scale: float, max_query_len: int, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """:func:`prefill` over an 8-bit cache: causal attention of each sequence's new tokens (their K/V already written)
+    over its context.  q: [N, Hq, d], float16 or bfloat16; other arguments as :func:`prefill`."""
+    from . import PagedAttentionError, _DTYPES, _check, _need_cuda, _stream, load_library
+    dev = k_cache.device
+    for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
+                    ("block_tables", block_tables), ("query_start", query_start), ("context_lens", context_lens)):
+        _need_cuda(name, t, dev)
+    nb, hkv, bs, d = fp8_geometry(k_cache, v_cache, k_scale, v_scale)
+    if q.dtype not in _DTYPES or q.dim() != 3:
+        raise PagedAttentionError("q must be float16 or bfloat16 [N, Hq, d]")
+    N, hq = q.shape[0], q.shape[1]
+    S = context_lens.shape[0]
+    qs = token_stride("q", q, (N, hq, d), q.dtype)
+    ts = _tables(block_tables, context_lens, S)
+    if query_start.dtype != torch.int32 or tuple(query_start.shape) != (S + 1,) or not query_start.is_contiguous():
+        raise PagedAttentionError("query_start must be a contiguous int32 [S + 1] tensor")
+    if out is None:
+        out = torch.empty((N, hq, d), dtype=q.dtype, device=dev)
+        os_ = hq * d
+    else:
+        _need_cuda("out", out, dev)
+        os_ = token_stride("out", out, (N, hq, d), q.dtype)
+    lib = load_library()
+    with on_device(dev):
+        stream = _stream(dev)
+        if workspace is None:
+            workspace = _scratch(dev, stream, int(lib.pa_prefill_fp8_workspace_size(S, N, hq, hkv, d, bs,
+                                                                                    int(max_query_len))))
+        elif not (workspace.is_cuda and workspace.device == dev and workspace.is_contiguous()):
+            raise PagedAttentionError("workspace must be a contiguous tensor on the caches' device")
+        rc = lib.pa_prefill_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                v_scale.data_ptr(), block_tables.data_ptr(), query_start.data_ptr(),
+                                context_lens.data_ptr(), float(scale), out.data_ptr(), S, N, hq, hkv, d, bs, nb,
+                                ts if S else 1, int(max_query_len), qs, os_, _DTYPES[q.dtype],
+                                workspace.data_ptr() if workspace is not None else None,
+                                workspace.numel() * workspace.element_size() if workspace is not None else 0, stream)
+    _check(rc, "pa_prefill_fp8")
     return out

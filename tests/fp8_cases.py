@@ -45,16 +45,18 @@ class Batch:
         return out
 
 
-def tolerance(out, mean_abs, dots, ctx_of, d, dtype, v_scale_max, p_half_step=2.0 ** -11):
-    """Elementwise bound of |kernel - exact|.
+def tolerance(out, mean_abs, dots, keys, d, dtype, v_max, p_half_step=2.0 ** -11, p_floor=2.0 ** -32, kv_half_step=0.0):
+    """Elementwise bound of |kernel - exact|; `keys`: context length of each row [N], `v_max`: the largest value the
+    cache's bytes can stand for (448 times the largest scale).
 
-    A weight w is off by a relative e: half a step of the type it is rounded to; the score's fp32 dot of d products
-    and its scaling, (d + 8) 2^-24 of sum |scale q k| in nats, taken twice for the running maximum's share; 2^-20
-    for the exponential's and logarithm's approximations.  Numerator and normaliser see the same w, so the output
-    moves by at most e (sum w |v| + |out|); their fp32 sums over L keys add L 2^-24 of each.  Weights below
-    2^-31 of the largest lose bits: L 2^-32 times the largest value the bytes can stand for.  Then half a step of
-    the output's type (2^-25 below fp16's normal range)."""
-    L = ctx_of[:, None, None]
-    e = p_half_step + 2 * (d + 8) * 2.0 ** -24 * dots[:, :, None] + 2.0 ** -20 + 2 * L * 2.0 ** -24
-    err = e * (mean_abs + np.abs(out)) + L * 2.0 ** -32 * 448.0 * v_scale_max
+    A weight w is off by a relative e: half a step of the type it is rounded to (p_half_step); the score's fp32 dot of
+    d products and its scaling, (d + 8) 2^-24 of sum |scale q k| in nats, taken twice for the running maximum's share;
+    what rounding K to the storage type moves it (kv_half_step of the same sum); 2^-20 for the exponential's and
+    logarithm's approximations.  Numerator and normaliser see the same w, so the output moves by at most
+    e (sum w |v| + |out|); their fp32 sums over L keys add L 2^-24 of each, rounded V kv_half_step of sum w |v|.
+    Weights too small for their type's normal numbers are off by p_floor of the largest: L p_floor v_max.  Then half a
+    step of the output's type (2^-25 below fp16's normal range)."""
+    L = np.asarray(keys, np.float64)[:, None, None]
+    e = p_half_step + (2 * (d + 8) * 2.0 ** -24 + 2 * kv_half_step) * dots[:, :, None] + 2.0 ** -20 + 2 * L * 2.0 ** -24
+    err = e * (mean_abs + np.abs(out)) + kv_half_step * mean_abs + L * p_floor * v_max
     return err + HALF_STEP[dtype] * (np.abs(out) + err) + 2.0 ** -25

@@ -30,7 +30,7 @@ def check(got, q, b, dtype, scale):
     k, v = b.values()
     out, mean_abs, dots = R.attention(q.double().numpy(), k, v, b.tables, b.ctx, scale, bounds=True)
     vs = float(np.nanmax(b.pools[3], initial=0.0))
-    tol = tolerance(out, mean_abs, dots, b.ctx.astype(np.float64), b.d, dtype, vs)
+    tol = tolerance(out, mean_abs, dots, b.ctx, b.d, dtype, 448.0 * vs)
     got = got.double().cpu().numpy()
     assert np.all(np.isfinite(got))
     err = np.abs(got - out)
