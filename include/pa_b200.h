@@ -544,6 +544,20 @@ int pa_prefill_fp8(const void *q, const void *k_cache, const void *v_cache, cons
                    int64_t num_blocks, int32_t block_table_stride, int32_t max_query_len, int64_t q_token_stride,
                    int64_t out_token_stride, int32_t dtype, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * pa_copy_blocks_fp8, pa_swap_blocks_fp8 -- pa_copy_blocks and pa_swap_blocks
+ * for 8-bit pools: a block's bytes move together with the K and V scales of
+ * its heads.  Rules, mapping and pinned host memory (scales included) as for
+ * the 16-bit calls.
+ */
+int pa_copy_blocks_fp8(void *k_cache, void *v_cache, float *k_scale, float *v_scale, const int64_t *block_mapping,
+                       int64_t num_pairs, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                       int64_t num_blocks, void *stream);
+int pa_swap_blocks_fp8(const void *src_k, const void *src_v, const float *src_k_scale, const float *src_v_scale,
+                       void *dst_k, void *dst_v, float *dst_k_scale, float *dst_v_scale,
+                       const int64_t *block_mapping, int64_t num_pairs, int32_t num_kv_heads, int32_t head_dim,
+                       int32_t block_size, int64_t src_num_blocks, int64_t dst_num_blocks, void *stream);
+
 /* pa_version -- library ABI version (major * 10000 + minor * 100 + patch). */
 int32_t pa_version(void);
 

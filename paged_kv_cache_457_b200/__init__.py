@@ -38,6 +38,7 @@ __all__ = [
     "DEV_ERR_PLAN", "find_prefix_groups", "cascade_plan", "cascade_workspace_size", "decode_cascade", "PrefixGroups",
     "CascadePlan", "DEV_ERR_POSITION", "rope_table", "rope_write_kv", "write_kv_fp8", "rope_write_kv_fp8",
     "decode_fp8", "decode_fp8_workspace_size", "prefill_fp8",
+    "copy_blocks_fp8", "swap_blocks_fp8",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -68,6 +69,7 @@ EXPORTED_SYMBOLS = (
     "pa_find_prefix_groups", "pa_cascade_plan", "pa_cascade_workspace_size", "pa_decode_cascade",
     "pa_rope_write_kv", "pa_write_kv_fp8", "pa_rope_write_kv_fp8",
     "pa_decode_fp8_workspace_size", "pa_decode_fp8", "pa_prefill_fp8_workspace_size", "pa_prefill_fp8",
+    "pa_copy_blocks_fp8", "pa_swap_blocks_fp8",
 )
 
 
@@ -368,6 +370,7 @@ def debug_wait_timeout(limit_ns: int = 10_000_000) -> None:
 
 from .block_manager import BlockManager, BlockManagerError, DecodeStepPlan, PrefillStepPlan  # noqa: E402
 from .append import rope_table, rope_write_kv, rope_write_kv_fp8, write_kv_fp8  # noqa: E402
-from .fp8 import decode_fp8, decode_fp8_workspace_size, prefill_fp8  # noqa: E402
+from .fp8 import (copy_blocks_fp8, decode_fp8, decode_fp8_workspace_size, prefill_fp8,  # noqa: E402
+                  swap_blocks_fp8)  # noqa: E402
 from .cascade import (CascadePlan, PrefixGroups, cascade_plan, cascade_workspace_size,  # noqa: E402
                       decode_cascade, find_prefix_groups)

@@ -740,6 +740,46 @@ int launch_decode8(const pa::Decode8Args &a, const LaunchPlan &lp, const CUtenso
                                : launch_pdl(pa::decode_merge_kernel<E, D, 1, 4>, grid, block, 0, stream, a.d));
 }
 
+// Block copies of 8-bit pools: blocks and the scales of their heads, in one launch.
+int swap_fp8(const void *const (&ptrs)[9], int64_t num_pairs, int32_t num_kv_heads, int32_t head_dim,
+             int32_t block_size, int64_t src_num_blocks, int64_t dst_num_blocks, cudaStream_t stream) {
+  if (num_pairs < 0 || num_kv_heads <= 0 || src_num_blocks <= 0 || dst_num_blocks <= 0) return PA_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
+  if (num_pairs == 0) return PA_OK;
+  // ptrs: source K, V, K scales, V scales, destination K, V, K scales, V scales, mapping
+  const void *view[9];
+  for (const void *p : ptrs)
+    if (!p) return PA_ERR_NULL;
+  for (int i = 0; i < 9; ++i) {
+    const uintptr_t mask = i == 8 ? 7u : (i & 2) ? 3u : 15u;
+    if (reinterpret_cast<uintptr_t>(ptrs[i]) & mask) return PA_ERR_ALIGN;
+  }
+  for (int i = 0; i < 9; ++i) {
+    const int rc = device_view(ptrs[i], &view[i]);
+    if (rc != PA_OK) return rc;
+  }
+  int sms = 0;
+  int rc = current_sms(&sms);
+  if (rc != PA_OK) return rc;
+  pa::CopyArgs a;
+  a.src_k = static_cast<const uint4 *>(view[0]);
+  a.src_v = static_cast<const uint4 *>(view[1]);
+  a.dst_k = static_cast<uint4 *>(const_cast<void *>(view[4]));
+  a.dst_v = static_cast<uint4 *>(const_cast<void *>(view[5]));
+  a.mapping = static_cast<const int64_t *>(view[8]);
+  a.num_pairs = num_pairs;
+  a.chunks_per_block = (long long)num_kv_heads * block_size * head_dim / 16;
+  a.src_blocks = src_num_blocks;
+  a.dst_blocks = dst_num_blocks;
+  const pa::CopyScales s{static_cast<const float *>(view[2]), static_cast<const float *>(view[3]),
+                         static_cast<float *>(const_cast<void *>(view[6])),
+                         static_cast<float *>(const_cast<void *>(view[7])), num_kv_heads};
+  const long long warp_tiles = num_pairs * 2 * ((a.chunks_per_block + pa::COPY_TILE - 1) / pa::COPY_TILE);
+  const int grid = (int)std::max(1LL, std::min<long long>((warp_tiles + 7) / 8, (long long)sms * 8));
+  return finish_launch(launch_pdl(pa::copy_blocks_fp8_kernel, dim3(grid), dim3(256), 0, stream, a, s));
+}
+
 int check_prefill8_shape(int32_t num_seqs, int64_t num_query_tokens, int32_t num_q_heads, int32_t num_kv_heads,
                          int32_t head_dim, int32_t block_size, int32_t max_query_len) {
   if (num_seqs < 0 || num_query_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_query_len < 0)
@@ -1359,6 +1399,24 @@ int pa_prefill(const void *q, const void *k_cache, const void *v_cache, const in
   }
   if (head_dim == 128) return launch(pa::prefill_tc_kernel<pa::F16, 128>, pa::PrefillSmem<128>::ALLOC);
   return launch(pa::prefill_tc_kernel<pa::F16, 64>, pa::PrefillSmem<64>::ALLOC);
+}
+
+int pa_swap_blocks_fp8(const void *src_k, const void *src_v, const float *src_k_scale, const float *src_v_scale,
+                       void *dst_k, void *dst_v, float *dst_k_scale, float *dst_v_scale,
+                       const int64_t *block_mapping, int64_t num_pairs, int32_t num_kv_heads, int32_t head_dim,
+                       int32_t block_size, int64_t src_num_blocks, int64_t dst_num_blocks, void *stream) {
+  const void *const ptrs[9] = {src_k, src_v, src_k_scale, src_v_scale, dst_k, dst_v, dst_k_scale, dst_v_scale,
+                               block_mapping};
+  return swap_fp8(ptrs, num_pairs, num_kv_heads, head_dim, block_size, src_num_blocks, dst_num_blocks,
+                  static_cast<cudaStream_t>(stream));
+}
+
+int pa_copy_blocks_fp8(void *k_cache, void *v_cache, float *k_scale, float *v_scale, const int64_t *block_mapping,
+                       int64_t num_pairs, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                       int64_t num_blocks, void *stream) {
+  const void *const ptrs[9] = {k_cache, v_cache, k_scale, v_scale, k_cache, v_cache, k_scale, v_scale, block_mapping};
+  return swap_fp8(ptrs, num_pairs, num_kv_heads, head_dim, block_size, num_blocks, num_blocks,
+                  static_cast<cudaStream_t>(stream));
 }
 
 size_t pa_prefill_fp8_workspace_size(int32_t num_seqs, int64_t num_query_tokens, int32_t num_q_heads,

@@ -27,11 +27,11 @@ struct CopyArgs {
 // A pair with a negative entry is skipped; one outside its pool is skipped
 // and flagged.  Either pool may be pinned host memory (unified addressing).
 constexpr int COPY_UNROLL = 4;
-constexpr int COPY_TILE = COPY_UNROLL * 32;  // chunks; every supported block is a multiple of it
+constexpr int COPY_TILE = COPY_UNROLL * 32;  // chunks; every supported 16-bit block is a multiple of it
 
-__global__ void __launch_bounds__(256) copy_blocks_kernel(const CopyArgs a) {
-  grid_dependency_wait();
-  grid_launch_dependents();
+// `scales(pair's source, destination, is_v)` is called once per pair and cache, by a whole warp.
+template <class F>
+__device__ __forceinline__ void copy_block_tiles(const CopyArgs &a, F scales) {
   const int lane = threadIdx.x & 31;
   const long long tiles_per_block = (a.chunks_per_block + COPY_TILE - 1) / COPY_TILE;
   const long long total = a.num_pairs * 2 * tiles_per_block;
@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(const CopyArgs a) {
       if (tile == 0 && !is_v && lane == 0) atomicOr(&g_status, PA_DEV_ERR_BLOCK_ID);
       continue;
     }
+    if (tile == 0) scales(src, dst, is_v);
     const long long base = tile * COPY_TILE + lane;
     const uint4 *from = (is_v ? a.src_v : a.src_k) + src * a.chunks_per_block;
     uint4 *to = (is_v ? a.dst_v : a.dst_k) + dst * a.chunks_per_block;
@@ -58,6 +59,29 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(const CopyArgs a) {
     for (int u = 0; u < COPY_UNROLL; ++u)
       if (base + u * 32 < a.chunks_per_block) to[base + u * 32] = v[u];
   }
+}
+
+__global__ void __launch_bounds__(256) copy_blocks_kernel(const CopyArgs a) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  copy_block_tiles(a, [](long long, long long, bool) {});
+}
+
+// Blocks of an 8-bit cache move with the scales of their heads.
+struct CopyScales {
+  const float *src_k, *src_v;
+  float *dst_k, *dst_v;
+  int num_kv_heads;
+};
+
+__global__ void __launch_bounds__(256) copy_blocks_fp8_kernel(const CopyArgs a, const CopyScales s) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  copy_block_tiles(a, [&](long long src, long long dst, bool is_v) {
+    const float *from = (is_v ? s.src_v : s.src_k) + src * s.num_kv_heads;
+    float *to = (is_v ? s.dst_v : s.dst_k) + dst * s.num_kv_heads;
+    for (int h = threadIdx.x & 31; h < s.num_kv_heads; h += 32) to[h] = from[h];
+  });
 }
 
 }  // namespace pa

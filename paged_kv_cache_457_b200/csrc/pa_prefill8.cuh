@@ -61,34 +61,37 @@ struct LoadUnit {
 
   // Rows tok0 .. tok0 + 31 of the item's context; p0, p1: physical blocks of the two halves (-1: past the context).
   __device__ __forceinline__ void load(const uint8_t *cache, const float *scale, const PrefillArgs &a, int h, int p0,
-                                       int p1, int tok0, int kmax, float factor, int lane) {
-    const int bs = a.block_size;
+                                       int p1, int tok0, int kmax, int lane) {
+    // the unit's two halves of 16 rows: blocks p0 and p1, or the two halves of block p0
     const long long slab0 = (long long)p0 * a.num_kv_heads + h, slab1 = (long long)p1 * a.num_kv_heads + h;
-    s[0] = p0 >= 0 ? __ldg(scale + slab0) * factor : 0.f;
-    s[1] = p1 >= 0 ? __ldg(scale + slab1) * factor : 0.f;
+    s[0] = p0 >= 0 ? __ldg(scale + slab0) : 0.f;
+    s[1] = p1 >= 0 ? __ldg(scale + slab1) : 0.f;
+    const int off = (lane / LPR) * D + (lane % LPR) * 16;
+    const uint8_t *half0 = cache + slab0 * a.block_size * D + off;
+    const uint8_t *half1 = cache + slab1 * a.block_size * D + (a.block_size == 16 ? 0 : 16 * D) + off;
+    const int live = kmax - tok0 - lane / LPR;  // rows of this lane's column that lie in the context
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int tok = tok0 + i * STEP + lane / LPR;
-      const long long slab = i < N / 2 ? slab0 : slab1;
-      w[i] = tok < kmax ? __ldg(reinterpret_cast<const uint4 *>(cache + (slab * bs + tok % bs) * D) + lane % LPR)
-                        : make_uint4(0, 0, 0, 0);
-    }
+    for (int i = 0; i < N; ++i)
+      w[i] = i * STEP < live ? __ldg(reinterpret_cast<const uint4 *>((i < N / 2 ? half0 : half1) + (i % (N / 2)) * STEP * D))
+                             : make_uint4(0, 0, 0, 0);
   }
   // Into rows row0 .. row0 + 31 of a tile stored as D / 64 regions of [128 rows][128 bytes], swizzled.
-  __device__ __forceinline__ void store(uint8_t *tile, int row0, int lane) const {
+  __device__ __forceinline__ void store(uint8_t *tile, int row0, float factor, int lane) const {
     const int cc = lane % LPR;  // dims 16 cc .. 16 cc + 15: chunks 2 cc and 2 cc + 1 of their 64-element region
     uint8_t *region = tile + (cc / 4) * 128 * 128;
     const int c0 = (cc % 4) * 2;
+    const float2 s0 = make_float2(s[0] * factor, s[0] * factor), s1 = make_float2(s[1] * factor, s[1] * factor);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float sc = s[i < N / 2 ? 0 : 1];
+      const float2 sc = i < N / 2 ? s0 : s1;
       const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
       uint32_t o[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 a = e4m3x2_to_float2((uint16_t)in[j]), b = e4m3x2_to_float2((uint16_t)(in[j] >> 16));
-        o[2 * j] = narrow2_sat<E>(a.x * sc, a.y * sc);
-        o[2 * j + 1] = narrow2_sat<E>(b.x * sc, b.y * sc);
+        const float2 a = __fmul2_rn(e4m3x2_to_float2((uint16_t)in[j]), sc);
+        const float2 b = __fmul2_rn(e4m3x2_to_float2((uint16_t)(in[j] >> 16)), sc);
+        o[2 * j] = narrow2_sat<E>(a.x, a.y);
+        o[2 * j + 1] = narrow2_sat<E>(b.x, b.y);
       }
       const int row = row0 + i * STEP + lane / LPR;
       uint8_t *dst = region + row * 128;
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
         const int p1 = a.block_size == 16 ? __shfl_sync(FULL, ent, (page + 1) & 31) : p0;
         const bool is_v = (u >> 2) & 1;
         x.load(is_v ? args.v_cache : args.k_cache, is_v ? args.v_scale : args.k_scale, a, it.h, p0, p1, tok0, it.kmax,
-               is_v ? 1.f : args.k_sign, lane);
+               lane);
       };
       const int units = it.nt * 8;
       const int u0 = (int)((w + PF8_LOADERS - (g * 8) % PF8_LOADERS) % PF8_LOADERS);
@@ -286,7 +289,7 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
           ok = false;
           break;
         }
-        cur.store(sm + (is_v ? L::V : L::K) + st * HALVES * REGION, (u & 3) * 32, lane);
+        cur.store(sm + (is_v ? L::V : L::K) + st * HALVES * REGION, (u & 3) * 32, is_v ? 1.f : args.k_sign, lane);
         fence_proxy_async_smem();  // the tensor cores read the rows through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive(&(is_v ? v_full : k_full)[st]);

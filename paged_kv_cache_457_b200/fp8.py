@@ -20,6 +20,8 @@ def bind(lib: ctypes.CDLL) -> None:
         "pa_prefill_fp8_workspace_size": (sz, [i32, i64, i32, i32, i32, i32, i32]),
         "pa_prefill_fp8": (ctypes.c_int, [vp] * 8 + [f32, vp, i32, i64] + [i32] * 4 + [i64, i32, i32, i64, i64, i32, vp,
                                                                                      sz, vp]),
+        "pa_copy_blocks_fp8": (ctypes.c_int, [vp] * 5 + [i64, i32, i32, i32, i64, vp]),
+        "pa_swap_blocks_fp8": (ctypes.c_int, [vp] * 9 + [i64, i32, i32, i32, i64, i64, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -141,3 +143,40 @@ def prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k
                                 workspace.numel() * workspace.element_size() if workspace is not None else 0, stream)
     _check(rc, "pa_prefill_fp8")
     return out
+
+
+def copy_blocks_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                    block_mapping: torch.Tensor) -> None:
+    """:func:`copy_blocks` for 8-bit caches: a block's bytes and the scales of its heads (copy-on-write)."""
+    from . import _check, _mapping, _need_cuda, _stream, load_library
+    dev = k_cache.device
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale)):
+        _need_cuda(name, t, dev)
+    nb, hkv, bs, d = fp8_geometry(k_cache, v_cache, k_scale, v_scale)
+    m = _mapping(block_mapping, dev)
+    with on_device(dev):
+        rc = load_library().pa_copy_blocks_fp8(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                               v_scale.data_ptr(), m.data_ptr(), m.shape[0], hkv, d, bs, nb,
+                                               _stream(dev))
+    _check(rc, "pa_copy_blocks_fp8")
+
+
+def swap_blocks_fp8(src_k: torch.Tensor, src_v: torch.Tensor, src_k_scale: torch.Tensor, src_v_scale: torch.Tensor,
+                    dst_k: torch.Tensor, dst_v: torch.Tensor, dst_k_scale: torch.Tensor, dst_v_scale: torch.Tensor,
+                    block_mapping: torch.Tensor, device: torch.device | None = None) -> None:
+    """:func:`swap_blocks` for 8-bit pools with their scales; either pool may be pinned host memory."""
+    from . import PagedAttentionError, _check, _mapping, _stream, load_library
+    pools = (src_k, src_v, src_k_scale, src_v_scale, dst_k, dst_v, dst_k_scale, dst_v_scale)
+    for t in pools:
+        if not (t.is_cuda or t.is_pinned()):
+            raise PagedAttentionError("every pool and scale must be on the GPU or in pinned host memory")
+    dev = device or next((t.device for t in pools if t.is_cuda), torch.device("cuda", torch.cuda.current_device()))
+    snb, hkv, bs, d = fp8_geometry(src_k, src_v, src_k_scale, src_v_scale)
+    dnb, *rest = fp8_geometry(dst_k, dst_v, dst_k_scale, dst_v_scale)
+    if tuple(rest) != (hkv, bs, d):
+        raise PagedAttentionError("pools must share heads, block size and head dim")
+    m = _mapping(block_mapping, dev)
+    with on_device(dev):
+        rc = load_library().pa_swap_blocks_fp8(*(t.data_ptr() for t in pools), m.data_ptr(), m.shape[0], hkv, d, bs,
+                                               snb, dnb, _stream(dev))
+    _check(rc, "pa_swap_blocks_fp8")
