@@ -5,15 +5,20 @@
 Argument marshalling only; the work is one launch of the library's CUDA kernels per call.
 8-bit caches are ``torch.float8_e4m3fn`` tensors ``[num_blocks, num_kv_heads, block_size, head_dim]``
 with float32 scales ``[num_blocks, num_kv_heads]``: a stored value stands for value * scale.
+
+A decode step's calls last a few microseconds on the GPU, so the checks here look at each property of
+a tensor once and build their messages only when one fails.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
 
+from . import PagedAttentionError, _DTYPES, _cache_geometry, _check, _need_cuda, load_library
+
 F8 = torch.float8_e4m3fn
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
 def bind(lib: ctypes.CDLL) -> None:
@@ -29,33 +34,62 @@ def bind(lib: ctypes.CDLL) -> None:
         f.argtypes = args
 
 
-def on_device(dev: torch.device):
-    """Makes ``dev`` current for a call when it is not already: the library launches on the current device."""
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def stream_of(dev: torch.device) -> int:
+    """The current stream of ``dev`` as the C ABI takes it."""
+    return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def on_device(dev: torch.device, f, *args) -> int:
+    """f(*args) with ``dev`` the current device: the library launches on the current one."""
+    if dev.index == torch.cuda.current_device():
+        return f(*args)
+    with torch.cuda.device(dev):
+        return f(*args)
+
+
+def need_cuda(**tensors) -> None:
+    """Refuses whatever is not a CUDA tensor on the device of the first one (None: an argument left out)."""
+    dev = None
+    for name, t in tensors.items():
+        if t is not None:
+            _need_cuda(name, t, dev)
+            dev = dev or t.device
+
+
+def same_device(k_cache, *tensors) -> torch.device | None:
+    """The CUDA device all of these tensors lie on, None if they do not (:func:`need_cuda` then says which)."""
+    try:
+        dev = k_cache.device
+        if dev.type != "cuda":
+            return None
+        for t in tensors:
+            if t is not None and t.device != dev:
+                return None
+        return dev
+    except AttributeError:
+        return None
 
 
 def fp8_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
     """Sizes (num_blocks, num_kv_heads, block_size, head_dim) of a checked 8-bit cache."""
-    from . import PagedAttentionError
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise PagedAttentionError("k_cache/v_cache must both be [num_blocks, num_kv_heads, block_size, head_dim]")
-    if k_cache.dtype != F8 or v_cache.dtype != F8:
+    if k_cache.dtype is not F8 or v_cache.dtype is not F8:
         raise PagedAttentionError("8-bit caches must be float8_e4m3fn")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise PagedAttentionError("caches must be contiguous")
-    shape = k_cache.shape[:2]
+    heads = shape[:2]
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+        if t.dtype is not torch.float32 or t.shape != heads or not t.is_contiguous():
             raise PagedAttentionError(f"{name} must be a contiguous float32 [num_blocks, num_kv_heads] tensor")
-    return tuple(k_cache.shape)
+    return shape
 
 
-def token_stride(name: str, t: torch.Tensor, shape, dtype) -> int:
+def token_stride(name: str, t: torch.Tensor, T: int, H: int, d: int, dtype) -> int:
     """Checks rows [T, H, d] (heads and dims contiguous within a token) and returns their token stride."""
-    from . import PagedAttentionError
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise PagedAttentionError(f"{name} must be {list(shape)} of {dtype}, not {list(t.shape)} of {t.dtype}")
-    T, H, d = shape
+    if t.dtype is not dtype or t.shape != (T, H, d):
+        raise PagedAttentionError(f"{name} must be {[T, H, d]} of {dtype}, not {list(t.shape)} of {t.dtype}")
     if T == 0:
         return H * d
     s0, s1, s2 = t.stride()
@@ -64,11 +98,11 @@ def token_stride(name: str, t: torch.Tensor, shape, dtype) -> int:
     return s0 if T > 1 else H * d
 
 
-def _slots(slot_mapping: torch.Tensor) -> int:
-    from . import PagedAttentionError
-    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
+def _tokens(slot_mapping: torch.Tensor) -> int:
+    shape = slot_mapping.shape
+    if slot_mapping.dtype is not torch.int64 or len(shape) != 1 or not slot_mapping.is_contiguous():
         raise PagedAttentionError("slot_mapping must be a contiguous int64 [T] tensor")
-    return int(slot_mapping.shape[0])
+    return shape[0]
 
 
 def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device=None) -> torch.Tensor:
@@ -81,29 +115,28 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, device=N
 
 
 def _rope_args(q, q_out, T, d, dtype, positions, cos_sin, dev):
-    """Checked (q_out, num_q_heads, q stride, q_out stride, rot_dim, max_positions)."""
-    from . import PagedAttentionError, _need_cuda
-    _need_cuda("positions", positions, dev)
-    _need_cuda("cos_sin", cos_sin, dev)
-    if positions.dtype != torch.int64 or tuple(positions.shape) != (T,) or not positions.is_contiguous():
+    """Checked (q pointer, q_out, its pointer, num_q_heads, q stride, q_out stride, rot_dim, max_positions)."""
+    if positions.dtype is not torch.int64 or positions.shape != (T,) or not positions.is_contiguous():
         raise PagedAttentionError("positions must be a contiguous int64 [T] tensor")
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+    angles = cos_sin.shape
+    if cos_sin.dtype is not torch.float32 or len(angles) != 2 or not cos_sin.is_contiguous():
         raise PagedAttentionError("cos_sin must be a contiguous float32 [max_positions, rot_dim] tensor")
-    max_positions, rot = cos_sin.shape
+    max_positions, rot = angles
     if q is None:
         if q_out is not None:
             raise PagedAttentionError("q_out without q")
-        return None, 0, 0, 0, rot, max_positions
-    _need_cuda("q", q, dev)
-    if q.dim() != 3 or q.shape[1] == 0:
+        return None, None, None, 0, 0, 0, rot, max_positions
+    shape = q.shape
+    if len(shape) != 3 or shape[1] == 0:
         raise PagedAttentionError("q must be [T, Hq, d]")
-    hq = q.shape[1]
-    qs = token_stride("q", q, (T, hq, d), dtype)
+    hq = shape[1]
+    qs = token_stride("q", q, T, hq, d, dtype)
     if q_out is None:
         q_out = torch.empty((T, hq, d), dtype=dtype, device=dev)
-        return q_out, hq, qs, hq * d, rot, max_positions
-    _need_cuda("q_out", q_out, dev)
-    return q_out, hq, qs, token_stride("q_out", q_out, (T, hq, d), dtype), rot, max_positions
+        qos = hq * d
+    else:
+        qos = token_stride("q_out", q_out, T, hq, d, dtype)
+    return q.data_ptr(), q_out, q_out.data_ptr(), hq, qs, qos, rot, max_positions
 
 
 def rope_write_kv(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -117,22 +150,20 @@ def rope_write_kv(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_ca
     A negative position marks padding: the token is left out altogether (its row of q_out is not written); a
     negative slot leaves out its K/V only.  ``q`` may be None.
     """
-    from . import _DTYPES, _cache_geometry, _check, _need_cuda, _stream, load_library
-    dev = k_cache.device
-    for name, t in (("k", k), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("slot_mapping", slot_mapping)):
-        _need_cuda(name, t, dev)
+    dev = same_device(k_cache, k, v, v_cache, slot_mapping, positions, cos_sin, q, q_out)
+    if dev is None:
+        need_cuda(k_cache=k_cache, k=k, v=v, v_cache=v_cache, slot_mapping=slot_mapping,
+                  positions=positions, cos_sin=cos_sin, q=q, q_out=q_out)
     nb, hkv, bs, d = _cache_geometry(k_cache, v_cache)
     dtype = k_cache.dtype
-    T = _slots(slot_mapping)
-    ks, vs = token_stride("k", k, (T, hkv, d), dtype), token_stride("v", v, (T, hkv, d), dtype)
-    q_out, hq, qs, qos, rot, maxp = _rope_args(q, q_out, T, d, dtype, positions, cos_sin, dev)
-    with on_device(dev):
-        rc = load_library().pa_rope_write_kv(
-            q.data_ptr() if hq else None, k.data_ptr(), v.data_ptr(), q_out.data_ptr() if hq else None,
-            k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
-            cos_sin.data_ptr(), T, hq, hkv, d, rot, 1 if interleaved else 0, bs, nb, maxp, qs, ks, vs, qos,
-            _DTYPES[dtype], _stream(dev))
-    _check(rc, "pa_rope_write_kv")
+    T = _tokens(slot_mapping)
+    ks, vs = token_stride("k", k, T, hkv, d, dtype), token_stride("v", v, T, hkv, d, dtype)
+    qp, q_out, qop, hq, qs, qos, rot, maxp = _rope_args(q, q_out, T, d, dtype, positions, cos_sin, dev)
+    rc = on_device(dev, load_library().pa_rope_write_kv, qp, k.data_ptr(), v.data_ptr(), qop, k_cache.data_ptr(),
+                   v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), T, hq, hkv, d,
+                   rot, 1 if interleaved else 0, bs, nb, maxp, qs, ks, vs, qos, _DTYPES[dtype], stream_of(dev))
+    if rc:
+        _check(rc, "pa_rope_write_kv")
     return q_out
 
 
@@ -144,22 +175,21 @@ def write_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     it starts anew when row 0 of the block is written and grows, with the block's bytes re-scaled, when a later
     row needs it.  The tokens of one block must stand together in ``slot_mapping`` (skipped ones may lie between).
     """
-    from . import PagedAttentionError, _DTYPES, _check, _need_cuda, _stream, load_library
-    dev = k_cache.device
-    for name, t in (("k", k), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale),
-                    ("v_scale", v_scale), ("slot_mapping", slot_mapping)):
-        _need_cuda(name, t, dev)
+    dev = same_device(k_cache, k, v, v_cache, k_scale, v_scale, slot_mapping)
+    if dev is None:
+        need_cuda(k_cache=k_cache, k=k, v=v, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                  slot_mapping=slot_mapping)
     nb, hkv, bs, d = fp8_geometry(k_cache, v_cache, k_scale, v_scale)
     dtype = k.dtype
     if dtype not in _DTYPES:
         raise PagedAttentionError("k and v must be float16 or bfloat16")
-    T = _slots(slot_mapping)
-    ks, vs = token_stride("k", k, (T, hkv, d), dtype), token_stride("v", v, (T, hkv, d), dtype)
-    with on_device(dev):
-        rc = load_library().pa_write_kv_fp8(
-            k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), slot_mapping.data_ptr(), T, hkv, d, bs, nb, ks, vs, _DTYPES[dtype], _stream(dev))
-    _check(rc, "pa_write_kv_fp8")
+    T = _tokens(slot_mapping)
+    ks, vs = token_stride("k", k, T, hkv, d, dtype), token_stride("v", v, T, hkv, d, dtype)
+    rc = on_device(dev, load_library().pa_write_kv_fp8, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+                   v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), slot_mapping.data_ptr(), T, hkv, d, bs,
+                   nb, ks, vs, _DTYPES[dtype], stream_of(dev))
+    if rc:
+        _check(rc, "pa_write_kv_fp8")
 
 
 def rope_write_kv_fp8(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
@@ -168,23 +198,21 @@ def rope_write_kv_fp8(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, 
                       interleaved: bool = False, q_out: torch.Tensor | None = None) -> torch.Tensor | None:
     """:func:`rope_write_kv` into 8-bit caches (scales as :func:`write_kv_fp8` keeps them); k is quantised from its
     fp32 rotation, the returned q has the type of q."""
-    from . import PagedAttentionError, _DTYPES, _check, _need_cuda, _stream, load_library
-    dev = k_cache.device
-    for name, t in (("k", k), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale),
-                    ("v_scale", v_scale), ("slot_mapping", slot_mapping)):
-        _need_cuda(name, t, dev)
+    dev = same_device(k_cache, k, v, v_cache, k_scale, v_scale, slot_mapping, positions, cos_sin, q, q_out)
+    if dev is None:
+        need_cuda(k_cache=k_cache, k=k, v=v, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                  slot_mapping=slot_mapping, positions=positions, cos_sin=cos_sin, q=q, q_out=q_out)
     nb, hkv, bs, d = fp8_geometry(k_cache, v_cache, k_scale, v_scale)
     dtype = k.dtype
     if dtype not in _DTYPES:
         raise PagedAttentionError("k and v must be float16 or bfloat16")
-    T = _slots(slot_mapping)
-    ks, vs = token_stride("k", k, (T, hkv, d), dtype), token_stride("v", v, (T, hkv, d), dtype)
-    q_out, hq, qs, qos, rot, maxp = _rope_args(q, q_out, T, d, dtype, positions, cos_sin, dev)
-    with on_device(dev):
-        rc = load_library().pa_rope_write_kv_fp8(
-            q.data_ptr() if hq else None, k.data_ptr(), v.data_ptr(), q_out.data_ptr() if hq else None,
-            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-            slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), T, hq, hkv, d, rot,
-            1 if interleaved else 0, bs, nb, maxp, qs, ks, vs, qos, _DTYPES[dtype], _stream(dev))
-    _check(rc, "pa_rope_write_kv_fp8")
+    T = _tokens(slot_mapping)
+    ks, vs = token_stride("k", k, T, hkv, d, dtype), token_stride("v", v, T, hkv, d, dtype)
+    qp, q_out, qop, hq, qs, qos, rot, maxp = _rope_args(q, q_out, T, d, dtype, positions, cos_sin, dev)
+    rc = on_device(dev, load_library().pa_rope_write_kv_fp8, qp, k.data_ptr(), v.data_ptr(), qop, k_cache.data_ptr(),
+                   v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), slot_mapping.data_ptr(),
+                   positions.data_ptr(), cos_sin.data_ptr(), T, hq, hkv, d, rot, 1 if interleaved else 0, bs, nb, maxp,
+                   qs, ks, vs, qos, _DTYPES[dtype], stream_of(dev))
+    if rc:
+        _check(rc, "pa_rope_write_kv_fp8")
     return q_out

@@ -8,7 +8,11 @@ import ctypes
 
 import torch
 
-from .append import fp8_geometry, on_device, token_stride
+from . import (PagedAttentionError, _DTYPES, _check, _mapping, _need_cuda, _workspace, _workspaces,
+               load_library)
+from .append import fp8_geometry, need_cuda, on_device, same_device, stream_of, token_stride
+
+PA_ERR_WORKSPACE = -7
 
 
 def bind(lib: ctypes.CDLL) -> None:
@@ -31,29 +35,45 @@ def bind(lib: ctypes.CDLL) -> None:
 
 def _tables(block_tables: torch.Tensor, context_lens: torch.Tensor, S: int) -> int:
     """Checks the batch's tables and lengths; returns the table's row stride."""
-    from . import PagedAttentionError
-    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != S \
-            or (block_tables.shape[1] > 1 and block_tables.stride(1) != 1):
+    shape = block_tables.shape
+    if block_tables.dtype is not torch.int32 or len(shape) != 2 or shape[0] != S:
         raise PagedAttentionError("block_tables must be int32 [S, max_blocks] with contiguous rows")
-    if context_lens.dtype != torch.int32 or tuple(context_lens.shape) != (S,) or not context_lens.is_contiguous():
+    s0, s1 = block_tables.stride()
+    if s1 != 1 and shape[1] > 1:
+        raise PagedAttentionError("block_tables must be int32 [S, max_blocks] with contiguous rows")
+    if context_lens.dtype is not torch.int32 or context_lens.shape != (S,) or not context_lens.is_contiguous():
         raise PagedAttentionError("context_lens must be a contiguous int32 [S] tensor")
-    # a single row's stride says nothing: its width is the capacity
-    return block_tables.stride(0) if S > 1 else block_tables.shape[1]
+    if S > 1 and s0 < shape[1]:
+        raise PagedAttentionError("rows of block_tables must not overlap")
+    return s0 if S > 1 else max(1, shape[1])
 
 
-def _scratch(dev: torch.device, stream: int, nbytes: int) -> torch.Tensor | None:
-    """Workspace of a call: kept per device and stream, but a capture gets its own from the graph's pool, since a
-    captured graph may be replayed beside other calls and must not share (or outlive) theirs."""
-    from . import _workspace
-    if nbytes and torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    return _workspace(dev, stream, nbytes)
+def _run(dev, what, size, call, workspace):
+    """call(workspace pointer, bytes, stream) with the caller's workspace, or with one kept per device and stream.
+    A capture gets its own, from the graph's pool: a captured graph may be replayed beside other calls and must
+    neither share theirs nor outlive it."""
+    stream = stream_of(dev)
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise PagedAttentionError("workspace must be a contiguous tensor on the caches' device")
+        rc = call(workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
+    elif torch.cuda.is_current_stream_capturing():
+        n = size()
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        rc = call(ws.data_ptr() if n else None, n, stream)
+    else:
+        ws = _workspaces.get((dev.index, stream))
+        rc = call(ws.data_ptr(), ws.numel(), stream) if ws is not None else call(None, 0, stream)
+        if rc == PA_ERR_WORKSPACE:
+            ws = _workspace(dev, stream, size())
+            rc = call(ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, stream)
+    if rc:
+        _check(rc, what)
 
 
 def decode_fp8_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
                               partition_tokens: int = 0) -> int:
-    """Device workspace bytes of :func:`decode_fp8` for these sizes on the current device (0 on bad input)."""
-    from . import load_library
+    """Device workspace bytes of :func:`decode_fp8` for these sizes on the current device (0: none, or bad input)."""
     return int(load_library().pa_decode_fp8_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                                                            max_context_len, partition_tokens))
 
@@ -64,40 +84,38 @@ def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """:func:`decode` over an 8-bit cache: attention of q ([S, Hq, d], float16 or bfloat16) over each sequence's
     context; returns out ([S, Hq, d], q's dtype).  Other arguments as :func:`decode`."""
-    from . import PagedAttentionError, _DTYPES, _check, _need_cuda, _stream, load_library
-    dev = k_cache.device
-    for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
-                    ("block_tables", block_tables), ("context_lens", context_lens)):
-        _need_cuda(name, t, dev)
+    dev = same_device(k_cache, q, v_cache, k_scale, v_scale, block_tables, context_lens)
+    if dev is None:
+        need_cuda(k_cache=k_cache, q=q, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                  block_tables=block_tables, context_lens=context_lens)
     nb, hkv, bs, d = fp8_geometry(k_cache, v_cache, k_scale, v_scale)
-    if q.dtype not in _DTYPES or q.dim() != 3:
+    dtype, shape = q.dtype, q.shape
+    if dtype not in _DTYPES or len(shape) != 3:
         raise PagedAttentionError("q must be float16 or bfloat16 [S, Hq, d]")
-    S, hq = q.shape[0], q.shape[1]
-    qs = token_stride("q", q, (S, hq, d), q.dtype)
+    S, hq = shape[0], shape[1]
+    qs = token_stride("q", q, S, hq, d, dtype)
     ts = _tables(block_tables, context_lens, S)
     if out is None:
-        out = torch.empty((S, hq, d), dtype=q.dtype, device=dev)
+        out = torch.empty((S, hq, d), dtype=dtype, device=dev)
         os_ = hq * d
     else:
         _need_cuda("out", out, dev)
-        os_ = token_stride("out", out, (S, hq, d), q.dtype)
+        os_ = token_stride("out", out, S, hq, d, dtype)
     if max_context_len is None:
-        max_context_len = int(context_lens.max().item()) if S else 0
+        max_context_len = context_lens.max().item() if S else 0
+    max_context_len, partition_tokens, scale = int(max_context_len), int(partition_tokens), float(scale)
     lib = load_library()
-    with on_device(dev):
-        stream = _stream(dev)
-        if workspace is None:
-            workspace = _scratch(dev, stream, int(lib.pa_decode_fp8_workspace_size(
-                S, hq, hkv, d, bs, int(max_context_len), int(partition_tokens))))
-        elif not (workspace.is_cuda and workspace.device == dev and workspace.is_contiguous()):
-            raise PagedAttentionError("workspace must be a contiguous tensor on the caches' device")
-        rc = lib.pa_decode_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                               v_scale.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), float(scale),
-                               out.data_ptr(), S, hq, hkv, d, bs, nb, ts if S else 1, int(max_context_len), qs, os_,
-                               int(partition_tokens), _DTYPES[q.dtype],
-                               workspace.data_ptr() if workspace is not None else None,
-                               workspace.numel() * workspace.element_size() if workspace is not None else 0, stream)
-    _check(rc, "pa_decode_fp8")
+
+    def call(ws, nbytes, stream):
+        return lib.pa_decode_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                 v_scale.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), scale,
+                                 out.data_ptr(), S, hq, hkv, d, bs, nb, ts, max_context_len, qs, os_,
+                                 partition_tokens, _DTYPES[dtype], ws, nbytes, stream)
+
+    def size():
+        return int(lib.pa_decode_fp8_workspace_size(S, hq, hkv, d, bs, max_context_len, partition_tokens))
+
+    on_device(dev, _run, dev, "pa_decode_fp8", size, call, workspace)
     return out
 
 
@@ -107,57 +125,51 @@ def prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k
                 workspace: torch.Tensor | None = None) -> torch.Tensor:
     """:func:`prefill` over an 8-bit cache: causal attention of each sequence's new tokens (their K/V already written)
     over its context.  q: [N, Hq, d], float16 or bfloat16; other arguments as :func:`prefill`."""
-    from . import PagedAttentionError, _DTYPES, _check, _need_cuda, _stream, load_library
-    dev = k_cache.device
-    for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
-                    ("block_tables", block_tables), ("query_start", query_start), ("context_lens", context_lens)):
-        _need_cuda(name, t, dev)
+    dev = same_device(k_cache, q, v_cache, k_scale, v_scale, block_tables, query_start, context_lens)
+    if dev is None:
+        need_cuda(k_cache=k_cache, q=q, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                  block_tables=block_tables, query_start=query_start, context_lens=context_lens)
     nb, hkv, bs, d = fp8_geometry(k_cache, v_cache, k_scale, v_scale)
-    if q.dtype not in _DTYPES or q.dim() != 3:
+    dtype, shape = q.dtype, q.shape
+    if dtype not in _DTYPES or len(shape) != 3:
         raise PagedAttentionError("q must be float16 or bfloat16 [N, Hq, d]")
-    N, hq = q.shape[0], q.shape[1]
+    N, hq = shape[0], shape[1]
     S = context_lens.shape[0]
-    qs = token_stride("q", q, (N, hq, d), q.dtype)
+    qs = token_stride("q", q, N, hq, d, dtype)
     ts = _tables(block_tables, context_lens, S)
-    if query_start.dtype != torch.int32 or tuple(query_start.shape) != (S + 1,) or not query_start.is_contiguous():
+    if query_start.dtype is not torch.int32 or query_start.shape != (S + 1,) or not query_start.is_contiguous():
         raise PagedAttentionError("query_start must be a contiguous int32 [S + 1] tensor")
     if out is None:
-        out = torch.empty((N, hq, d), dtype=q.dtype, device=dev)
+        out = torch.empty((N, hq, d), dtype=dtype, device=dev)
         os_ = hq * d
     else:
         _need_cuda("out", out, dev)
-        os_ = token_stride("out", out, (N, hq, d), q.dtype)
+        os_ = token_stride("out", out, N, hq, d, dtype)
+    max_query_len, scale = int(max_query_len), float(scale)
     lib = load_library()
-    with on_device(dev):
-        stream = _stream(dev)
-        if workspace is None:
-            workspace = _scratch(dev, stream, int(lib.pa_prefill_fp8_workspace_size(S, N, hq, hkv, d, bs,
-                                                                                    int(max_query_len))))
-        elif not (workspace.is_cuda and workspace.device == dev and workspace.is_contiguous()):
-            raise PagedAttentionError("workspace must be a contiguous tensor on the caches' device")
-        rc = lib.pa_prefill_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                                v_scale.data_ptr(), block_tables.data_ptr(), query_start.data_ptr(),
-                                context_lens.data_ptr(), float(scale), out.data_ptr(), S, N, hq, hkv, d, bs, nb,
-                                ts if S else 1, int(max_query_len), qs, os_, _DTYPES[q.dtype],
-                                workspace.data_ptr() if workspace is not None else None,
-                                workspace.numel() * workspace.element_size() if workspace is not None else 0, stream)
-    _check(rc, "pa_prefill_fp8")
+
+    def call(ws, nbytes, stream):
+        return lib.pa_prefill_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                  v_scale.data_ptr(), block_tables.data_ptr(), query_start.data_ptr(),
+                                  context_lens.data_ptr(), scale, out.data_ptr(), S, N, hq, hkv, d, bs, nb, ts,
+                                  max_query_len, qs, os_, _DTYPES[dtype], ws, nbytes, stream)
+
+    def size():
+        return int(lib.pa_prefill_fp8_workspace_size(S, N, hq, hkv, d, bs, max_query_len))
+
+    on_device(dev, _run, dev, "pa_prefill_fp8", size, call, workspace)
     return out
 
 
 def copy_blocks_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                     block_mapping: torch.Tensor) -> None:
     """:func:`copy_blocks` for 8-bit caches: a block's bytes and the scales of its heads (copy-on-write)."""
-    from . import _check, _mapping, _need_cuda, _stream, load_library
+    need_cuda(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
     dev = k_cache.device
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale)):
-        _need_cuda(name, t, dev)
     nb, hkv, bs, d = fp8_geometry(k_cache, v_cache, k_scale, v_scale)
     m = _mapping(block_mapping, dev)
-    with on_device(dev):
-        rc = load_library().pa_copy_blocks_fp8(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                                               v_scale.data_ptr(), m.data_ptr(), m.shape[0], hkv, d, bs, nb,
-                                               _stream(dev))
+    rc = on_device(dev, load_library().pa_copy_blocks_fp8, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                   v_scale.data_ptr(), m.data_ptr(), m.shape[0], hkv, d, bs, nb, stream_of(dev))
     _check(rc, "pa_copy_blocks_fp8")
 
 
@@ -165,7 +177,6 @@ def swap_blocks_fp8(src_k: torch.Tensor, src_v: torch.Tensor, src_k_scale: torch
                     dst_k: torch.Tensor, dst_v: torch.Tensor, dst_k_scale: torch.Tensor, dst_v_scale: torch.Tensor,
                     block_mapping: torch.Tensor, device: torch.device | None = None) -> None:
     """:func:`swap_blocks` for 8-bit pools with their scales; either pool may be pinned host memory."""
-    from . import PagedAttentionError, _check, _mapping, _stream, load_library
     pools = (src_k, src_v, src_k_scale, src_v_scale, dst_k, dst_v, dst_k_scale, dst_v_scale)
     for t in pools:
         if not (t.is_cuda or t.is_pinned()):
@@ -176,7 +187,6 @@ def swap_blocks_fp8(src_k: torch.Tensor, src_v: torch.Tensor, src_k_scale: torch
     if tuple(rest) != (hkv, bs, d):
         raise PagedAttentionError("pools must share heads, block size and head dim")
     m = _mapping(block_mapping, dev)
-    with on_device(dev):
-        rc = load_library().pa_swap_blocks_fp8(*(t.data_ptr() for t in pools), m.data_ptr(), m.shape[0], hkv, d, bs,
-                                               snb, dnb, _stream(dev))
+    rc = on_device(dev, load_library().pa_swap_blocks_fp8, *(t.data_ptr() for t in pools), m.data_ptr(), m.shape[0], hkv,
+                   d, bs, snb, dnb, stream_of(dev))
     _check(rc, "pa_swap_blocks_fp8")
