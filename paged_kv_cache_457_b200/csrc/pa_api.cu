@@ -551,6 +551,7 @@ int static_workspace_address(void **addr) {
 // Checks shared by the appends; `rope`: positions, angles and q take part.
 int check_append(const pa::AppendArgs &a, int head_dim, int dtype, bool rope, bool fp8) {
   if (a.num_tokens < 0 || a.num_kv_heads <= 0 || a.num_blocks <= 0 || a.num_q_heads < 0) return PA_ERR_SHAPE;
+  if (fp8 && a.num_blocks > 0x7fffffffLL) return PA_ERR_SHAPE;
   if (dtype != PA_FLOAT16 && dtype != PA_BFLOAT16) return PA_ERR_DTYPE;
   if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
   if (a.block_size != 16 && a.block_size != 32) return PA_ERR_UNSUPPORTED;
@@ -612,10 +613,16 @@ int append_fp8(pa::AppendArgs &a, int head_dim, int dtype, bool rope, bool inter
   rc = current_sms(&sms);
   if (rc != PA_OK) return rc;
   // One token per warp while that keeps the warps of a few waves busy (a decode step: every token its own block);
-  // from there on block_size tokens per warp, about one run each, instead of many warps that find no run to own.
-  const long long per = 2LL * a.num_kv_heads;
-  a.tokens_per_warp = a.num_tokens * per > (long long)sms * 64 * 4 ? a.block_size : 1;
-  const long long warps = (a.num_tokens + a.tokens_per_warp - 1) / a.tokens_per_warp * per;
+  // from there on block_size tokens per warp, about one run each, and as many of its heads as still leave every SM
+  // several rounds of warps (the run is found once for them).
+  const long long pairs = 2LL * a.num_kv_heads;
+  a.tokens_per_warp = a.num_tokens * pairs > (long long)sms * 64 * 4 ? a.block_size : 1;
+  const long long stretches = (a.num_tokens + a.tokens_per_warp - 1) / a.tokens_per_warp;
+  a.heads_per_warp = 1;
+  while (a.tokens_per_warp > 1 && a.heads_per_warp < 4 &&
+         stretches * (pairs / (2 * a.heads_per_warp)) >= (long long)sms * 32)
+    a.heads_per_warp *= 2;
+  const long long warps = stretches * ((pairs + a.heads_per_warp - 1) / a.heads_per_warp);
   a.kv_blocks = (warps + 7) / 8;
   a.tokens_per_cta = row_tokens_per_cta(a.num_tokens, sms);
   const long long rows = a.num_q_heads > 0 ? (a.num_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta : 0;

@@ -36,6 +36,7 @@ struct AppendArgs {
   int num_q_heads, num_kv_heads, block_size, rot_dim;
   int tokens_per_cta;         // row part: consecutive tokens of one block of threads
   int tokens_per_warp;        // append_fp8_kernel: consecutive tokens of one warp (1 or block_size)
+  int heads_per_warp;         // append_fp8_kernel: (kv head, K or V) pairs of one warp
 };
 
 // ---------------------------------------------------------------- e4m3
@@ -100,6 +101,8 @@ __device__ __forceinline__ Angles load_angles(const AppendArgs &a, long long p, 
 // Turns the unit's 16 elements (chunks lo and hi) in place.
 template <bool INTERLEAVED>
 __device__ __forceinline__ void turn(float (&lo)[8], float (&hi)[8], const Angles &g) {
+  // Scalar products and sums: the packed forms (f32x2) come out contracted into fused ones, whatever their rounding
+  // suffix.
   auto pair = [&](float &x, float &y, int i) {
     const float xc = __fmul_rn(x, g.c[i]), ys = __fmul_rn(y, g.s[i]);
     const float yc = __fmul_rn(y, g.c[i]), xs = __fmul_rn(x, g.s[i]);
@@ -213,13 +216,13 @@ __global__ void __launch_bounds__(256) rope_write_kv_kernel(const AppendArgs a) 
 //   s_new = pow2_scale(amax) if the run holds the block's row 0 (the block starts anew), else
 //           max(s_old, pow2_scale(amax)); where s_new > s_old the block's bytes become rn(byte * s_old / s_new),
 //   bytes = rn_sat(x' / s_new) to the run's rows.
-// Rows are read in windows of BS tokens, kept in registers (2-byte values) between the two steps; a run is one
-// window unless skipped tokens or a slot named twice stretch it, and only then are rows read twice.
+// Rows are read in windows of BS tokens and kept in registers (2-byte values) between the two steps; a run is one
+// window unless skipped tokens or a slot named twice stretch it, and only then are rows read twice.  Kept in fp32,
+// rotated, they would save the second rotation but spill (64 registers more).
 
 // Token t of the call: its block (-1: not written), row in the block and position.  `flags`: set the status bits.
 template <int BS, bool ROPE>
-__device__ __forceinline__ long long append_token(const AppendArgs &a, long long t, bool flags, int &row,
-                                                  long long &pos) {
+__device__ __forceinline__ int append_token(const AppendArgs &a, long long t, bool flags, int &row, long long &pos) {
   row = -1;
   pos = 0;
   if (t < 0 || t >= a.num_tokens) return -1;
@@ -230,9 +233,15 @@ __device__ __forceinline__ long long append_token(const AppendArgs &a, long long
   if (flags && slot_high) atomicOr(&g_status, PA_DEV_ERR_SLOT);
   if (flags && pos_high) atomicOr(&g_status, PA_DEV_ERR_POSITION);
   if (slot < 0 || slot_high || pos_high) return -1;
-  const long long b = slot / BS;
-  row = (int)(slot - b * BS);
-  return b;
+  row = (int)(slot % BS);
+  return (int)(slot / BS);  // num_blocks is at most 2^31 - 1
+}
+
+// The largest of |f[i]| and m; NaN counts as nothing.
+__device__ __forceinline__ float amax8(const float (&f)[8], float m) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) m = fmaxf(fmaxf(m, fabsf(f[i])), fabsf(f[i + 1]));
+  return m;
 }
 
 template <class E, int D, int BS, bool INTERLEAVED, bool ROPE>
@@ -240,78 +249,86 @@ struct RunWindow {
   static constexpr int LPR = D / 16;    // lanes (units) of a row
   static constexpr int RPI = 32 / LPR;  // rows of one pass of the warp
   static constexpr int PASSES = BS / RPI;
+  static constexpr int ROWS = BS;
   uint4 w[PASSES][2];
   int my_row;        // lane i: row of the window's token i in the block, -1: none of the run's
   long long my_pos;
-  int grp, c;
-  bool turned;
-  Unit u;
+  unsigned live;     // lanes with such a row
 
-  __device__ __forceinline__ void setup(const AppendArgs &a, bool is_v, int lane) {
-    grp = lane / LPR;
-    c = lane % LPR;
-    turned = ROPE && !is_v;
-    u = turned ? unit_of<INTERLEAVED>(c, a.rot_dim) : Unit{2 * c, 2 * c + 1, false};
-  }
-  // Tokens ts .. ts + BS - 1 of the run [ts, te) of block blk.
-  __device__ __forceinline__ void load(const AppendArgs &a, const uint16_t *base, long long stride, long long ts,
-                                       long long te, long long blk, int lane) {
-    const long long b = append_token<BS, ROPE>(a, lane < BS && ts + lane < te ? ts + lane : -1, false, my_row, my_pos);
+  // Tokens ts .. ts + ROWS - 1 of the run [ts, te) of block blk.
+  __device__ __forceinline__ void tokens(const AppendArgs &a, long long ts, long long te, int blk, int lane) {
+    const int b = append_token<BS, ROPE>(a, lane < ROWS && ts + lane < te ? ts + lane : -1, false, my_row, my_pos);
     if (b != blk) my_row = -1;
+    live = __ballot_sync(FULL, my_row >= 0);
+  }
+  // The window's rows from `base` (token ts, this head).
+  __device__ __forceinline__ void load(const uint16_t *base, long long stride, const Unit &u, int lane) {
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-      const int r = p * RPI + grp;
-      const bool live = __shfl_sync(FULL, my_row, r) >= 0;
       w[p][0] = w[p][1] = make_uint4(0, 0, 0, 0);
-      if (live) {
-        const uint16_t *src = base + (ts + r) * stride;
+      const int r = p * RPI + lane / LPR;
+      if ((live >> r) & 1u) {
+        const uint16_t *src = base + r * stride;
         w[p][0] = __ldg(reinterpret_cast<const uint4 *>(src + u.c0 * 8));
         w[p][1] = __ldg(reinterpret_cast<const uint4 *>(src + u.c1 * 8));
       }
     }
   }
-  // This lane's 16 values of pass p in fp32 (the angles come from L1 the second time).
-  __device__ __forceinline__ void values(const AppendArgs &a, int p, float (&lo)[8], float (&hi)[8]) const {
+  // This lane's 16 values of pass p in fp32, rotated when `turned` (the angles come from L1 the second time).
+  __device__ __forceinline__ void values(const AppendArgs &a, int p, const Unit &u, bool turned, int lane,
+                                         float (&lo)[8], float (&hi)[8]) const {
     E::widen8(w[p][0], lo);
     E::widen8(w[p][1], hi);
     if (turned) {
-      const int r = p * RPI + grp;
+      const int r = p * RPI + lane / LPR;
       const long long pos = __shfl_sync(FULL, my_pos, r);
-      const bool live = __shfl_sync(FULL, my_row, r) >= 0;
-      if (u.rotated && live) turn<INTERLEAVED>(lo, hi, load_angles(a, pos, c));
+      if (u.rotated && ((live >> r) & 1u)) turn<INTERLEAVED>(lo, hi, load_angles(a, pos, lane % LPR));
     }
   }
   // Largest finite magnitude of this lane's values.
-  __device__ __forceinline__ float amax(const AppendArgs &a, unsigned live_rows) const {
+  __device__ __forceinline__ float amax(const AppendArgs &a, const Unit &u, bool turned, int lane) const {
     float m = 0.f;
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-      if ((live_rows >> (p * RPI)) == 0) break;
+      if ((live >> (p * RPI)) == 0) break;
       float lo[8], hi[8];
-      values(a, p, lo, hi);
+      values(a, p, u, turned, lane, lo, hi);
+      const float all = amax8(hi, amax8(lo, 0.f));
+      if (all < INFINITY) {
+        m = fmaxf(m, all);
+      } else {  // infinite values do not count
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = fabsf(lo[i]), y = fabsf(hi[i]);
-        m = fmaxf(m, x < INFINITY ? x : 0.f);
-        m = fmaxf(m, y < INFINITY ? y : 0.f);
+        for (int i = 0; i < 8; ++i) {
+          const float x = fabsf(lo[i]), y = fabsf(hi[i]);
+          m = fmaxf(m, fmaxf(x < INFINITY ? x : 0.f, y < INFINITY ? y : 0.f));
+        }
       }
     }
     return m;
   }
-  __device__ __forceinline__ void store(const AppendArgs &a, uint8_t *slab, float s, unsigned live_rows) const {
+  __device__ __forceinline__ void store(const AppendArgs &a, uint8_t *slab, const Unit &u, bool turned, float s,
+                                        int lane) const {
     // x / s: by the exact reciprocal where s is a power of two (always, unless the caller's own scale stands)
     const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
     const float inv = __fdiv_rn(1.f, s);
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-      if ((live_rows >> (p * RPI)) == 0) break;
+      if ((live >> (p * RPI)) == 0) break;
       float lo[8], hi[8];
-      values(a, p, lo, hi);
-      const int row = __shfl_sync(FULL, my_row, p * RPI + grp);
+      values(a, p, u, turned, lane, lo, hi);
+      const int row = __shfl_sync(FULL, my_row, p * RPI + lane / LPR);
+      if (pow2) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        lo[i] = pow2 ? __fmul_rn(lo[i], inv) : __fdiv_rn(lo[i], s);
-        hi[i] = pow2 ? __fmul_rn(hi[i], inv) : __fdiv_rn(hi[i], s);
+        for (int i = 0; i < 8; ++i) {
+          lo[i] = __fmul_rn(lo[i], inv);
+          hi[i] = __fmul_rn(hi[i], inv);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          lo[i] = __fdiv_rn(lo[i], s);
+          hi[i] = __fdiv_rn(hi[i], s);
+        }
       }
       uint2 b0, b1;
       b0.x = to_e4m3x2(lo[0], lo[1]) | (to_e4m3x2(lo[2], lo[3]) << 16);
@@ -326,116 +343,162 @@ struct RunWindow {
   }
 };
 
+// Rows of earlier calls in units of a larger scale: bytes b become rn(b * ratio).
+template <int BYTES>
+__device__ __forceinline__ void rescale_slab(uint8_t *slab, float ratio, int lane) {
+  const float2 r2 = make_float2(ratio, ratio);
+  uint4 *b = reinterpret_cast<uint4 *>(slab) + lane;
+  uint4 x[BYTES / 512];
+#pragma unroll
+  for (int i = 0; i < BYTES / 512; ++i) x[i] = b[i * 32];
+#pragma unroll
+  for (int i = 0; i < BYTES / 512; ++i) {
+    const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f0 = __fmul2_rn(e4m3x2_to_float2((uint16_t)in[j]), r2);
+      const float2 f1 = __fmul2_rn(e4m3x2_to_float2((uint16_t)(in[j] >> 16)), r2);
+      out[j] = to_e4m3x2(f0.x, f0.y) | (to_e4m3x2(f1.x, f1.y) << 16);
+    }
+    b[i * 32] = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
+// One run for one kv head of K or V.  `win` holds the run's first window of tokens.
 template <class E, int D, int BS, bool INTERLEAVED, bool ROPE>
-__device__ __forceinline__ void append_run(const AppendArgs &a, bool is_v, int h, long long ts, long long te,
-                                           long long blk, int lane) {
+__device__ __forceinline__ void append_run(const AppendArgs &a, RunWindow<E, D, BS, INTERLEAVED, ROPE> &win, bool is_v,
+                                           int h, long long ts, long long te, int blk, bool fresh, int lane) {
+  constexpr int ROWS = RunWindow<E, D, BS, INTERLEAVED, ROPE>::ROWS;
   if (!dcheck(blk >= 0 && blk < a.num_blocks && h < a.num_kv_heads)) return;
-  const uint16_t *base = (is_v ? a.v : a.k) + (long long)h * D;
+  const bool turned = ROPE && !is_v;
+  const int c = lane % (D / 16);
+  const Unit u = turned ? unit_of<INTERLEAVED>(c, a.rot_dim) : Unit{2 * c, 2 * c + 1, false};
   const long long stride = is_v ? a.v_stride : a.k_stride;
-  float *scale = (is_v ? a.v_scale : a.k_scale) + blk * a.num_kv_heads + h;
-  uint8_t *slab = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + (blk * a.num_kv_heads + h) * BS * D;
+  const uint16_t *base = (is_v ? a.v : a.k) + ts * stride + (long long)h * D;
+  const long long head = (long long)blk * a.num_kv_heads + h;
+  float *scale = (is_v ? a.v_scale : a.k_scale) + head;
+  uint8_t *slab = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + head * BS * D;
   const float s_old = *scale;
-  RunWindow<E, D, BS, INTERLEAVED, ROPE> win;
-  win.setup(a, is_v, lane);
-  float amax = 0.f;
-  bool fresh = false;
-  unsigned live = 0;
-  for (long long t = ts; t < te; t += BS) {
-    win.load(a, base, stride, t, te, blk, lane);
-    live = __ballot_sync(FULL, win.my_row >= 0);
-    amax = fmaxf(amax, win.amax(a, live));
-    fresh |= __any_sync(FULL, win.my_row == 0);
+  win.load(base, stride, u, lane);
+  float amax = win.amax(a, u, turned, lane);
+  const bool one = te - ts <= ROWS;
+  if (!one) {
+    for (long long t = ts + ROWS; t < te; t += ROWS) {
+      win.tokens(a, t, te, blk, lane);
+      win.load(base + (t - ts) * stride, stride, u, lane);
+      amax = fmaxf(amax, win.amax(a, u, turned, lane));
+    }
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, off));
   const float want = pow2_scale(amax);
   const float s_new = fresh ? want : fmaxf(s_old, want);
-
-  if (!fresh && s_new > s_old) {  // rows of earlier calls, in units of the larger scale
-    const float ratio = __fdiv_rn(s_old, s_new);
-    uint4 *b = reinterpret_cast<uint4 *>(slab);
-#pragma unroll
-    for (int i = 0; i < BS * D / 512; ++i) {
-      const uint4 x = b[i * 32 + lane];
-      const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-      uint32_t out[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f0 = e4m3x2_to_float2((uint16_t)in[j]), f1 = e4m3x2_to_float2((uint16_t)(in[j] >> 16));
-        out[j] = to_e4m3x2(__fmul_rn(f0.x, ratio), __fmul_rn(f0.y, ratio)) |
-                 (to_e4m3x2(__fmul_rn(f1.x, ratio), __fmul_rn(f1.y, ratio)) << 16);
-      }
-      b[i * 32 + lane] = make_uint4(out[0], out[1], out[2], out[3]);
-    }
+  if (!fresh && s_new > s_old) {
+    rescale_slab<BS * D>(slab, __fdiv_rn(s_old, s_new), lane);
     __syncwarp();  // before the run's own rows are written over theirs
   }
-  if (te - ts <= BS) {
-    win.store(a, slab, s_new, live);
+  if (one) {
+    win.store(a, slab, u, turned, s_new, lane);
   } else {
-    for (long long t = ts; t < te; t += BS) {
-      win.load(a, base, stride, t, te, blk, lane);
-      win.store(a, slab, s_new, __ballot_sync(FULL, win.my_row >= 0));
+    for (long long t = ts; t < te; t += ROWS) {
+      win.tokens(a, t, te, blk, lane);
+      win.load(base + (t - ts) * stride, stride, u, lane);
+      win.store(a, slab, u, turned, s_new, lane);
       __syncwarp();
     }
+    win.tokens(a, ts, te, blk, lane);  // as it was, for the run's next head
   }
   if (lane == 0) *scale = s_new;
 }
 
-// K/V part: warp w of the part takes tokens [i * tokens_per_warp, +tokens_per_warp) of one kv head of K or V, and
-// the runs that START among them (a run's later tokens may lie in the next warps' stretches, which then leave
-// them alone).  Row part (grid blocks from kv_blocks on): the q heads.
+// K/V part: warp w of the part takes tokens [i * tokens_per_warp, +tokens_per_warp) of heads_per_warp (kv head, K or
+// V) pairs, and the runs that START among them (a run's later tokens may lie in the next warps' stretches, which then
+// leave them alone).  Row part (grid blocks from kv_blocks on): the q heads.
 template <class E, int D, int BS, bool INTERLEAVED, bool ROPE>
-__global__ void __launch_bounds__(256) append_fp8_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(256, BS * D <= 2048 ? 2 : 1) append_fp8_kernel(const AppendArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
   if (ROPE && (long long)blockIdx.x >= a.kv_blocks) {
     append_row_block<E, D, INTERLEAVED>(a, (long long)blockIdx.x - a.kv_blocks, a.num_q_heads);
     return;
   }
+  using Window = RunWindow<E, D, BS, INTERLEAVED, ROPE>;
   const int lane = threadIdx.x & 31;
   const long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int per = 2 * a.num_kv_heads;
+  const int pairs = 2 * a.num_kv_heads;
+  const int per = (pairs + a.heads_per_warp - 1) / a.heads_per_warp;  // warps of a stretch
   const long long t0 = (w / per) * a.tokens_per_warp;
   if (t0 >= a.num_tokens) return;
-  const int hw = (int)(w % per);
-  const bool is_v = hw >= a.num_kv_heads;
-  const int h = is_v ? hw - a.num_kv_heads : hw;
+  const int hw0 = (int)(w % per);
+  // The stretch and its neighbours in one load: lane i holds token tb + i, the stretch is lanes [lead, lead + its
+  // length).  Most runs are settled by what the lanes hold; the loops below are for longer ones.
+  const int lead = (32 - a.tokens_per_warp) / 2;
+  const long long tb = t0 - lead;
   int row;
   long long pos;
-  const long long mine =
-      append_token<BS, ROPE>(a, lane < a.tokens_per_warp ? t0 + lane : -1, hw == 0, row, pos);
-  const unsigned written = __ballot_sync(FULL, mine >= 0);
-  if (!written) return;
-  // block of the last written token before this stretch (-1: none)
-  long long before = -1;
-  for (long long t = t0 - 1; t >= 0; t -= 32) {
-    const long long b = append_token<BS, ROPE>(a, t - lane, false, row, pos);
-    const unsigned m = __ballot_sync(FULL, b >= 0);
-    if (m) {
-      before = __shfl_sync(FULL, b, __ffs(m) - 1);
-      break;
+  const bool inside = lane >= lead && lane < lead + a.tokens_per_warp;
+  const int blk_l = append_token<BS, ROPE>(a, tb + lane, hw0 == 0 && inside, row, pos);
+  const unsigned written = __ballot_sync(FULL, blk_l >= 0);
+  const unsigned stretch = __ballot_sync(FULL, inside && blk_l >= 0);
+  if (!stretch) return;
+  // block of the last written token before the lanes' first, where the stretch's first written token needs it
+  int before = -1;
+  if ((written & ((1u << (__ffs(stretch) - 1)) - 1u)) == 0) {
+    for (long long t = tb - 1; t >= 0; t -= 32) {
+      int r;
+      long long p;
+      const int b = append_token<BS, ROPE>(a, t - lane, false, r, p);
+      const unsigned m = __ballot_sync(FULL, b >= 0);
+      if (m) {
+        before = __shfl_sync(FULL, b, __ffs(m) - 1);
+        break;
+      }
     }
   }
   // a written token starts a run where the written token before it lies in another block
   const unsigned below = written & ((1u << lane) - 1u);
-  const long long prev = __shfl_sync(FULL, mine, below ? 31 - __clz(below) : 0);
-  unsigned heads = __ballot_sync(FULL, mine >= 0 && mine != (below ? prev : before));
+  const int prev = __shfl_sync(FULL, blk_l, below ? 31 - __clz(below) : 0);
+  unsigned heads = __ballot_sync(FULL, inside && blk_l >= 0 && blk_l != (below ? prev : before));
   while (heads) {
     const int i = __ffs(heads) - 1;
     heads &= heads - 1;
-    const long long blk = __shfl_sync(FULL, mine, i);
-    const long long ts = t0 + i;
+    const int blk = __shfl_sync(FULL, blk_l, i);
+    const long long ts = tb + i;
     // the run ends before the next written token of another block; `te` is one past its last token
-    long long te = ts + 1;
-    for (long long t = ts + 1; t < a.num_tokens; t += 32) {
-      const long long b = append_token<BS, ROPE>(a, t + lane, false, row, pos);
-      const unsigned other = __ballot_sync(FULL, b >= 0 && b != blk);
-      unsigned same = __ballot_sync(FULL, b == blk);
-      if (other) same &= (other & (0u - other)) - 1u;  // those before the first of another block
-      if (same) te = t + 32 - __clz(same);
-      if (other) break;
+    unsigned other = __ballot_sync(FULL, lane > i && blk_l >= 0 && blk_l != blk);
+    unsigned same = __ballot_sync(FULL, lane >= i && blk_l == blk);
+    if (other) same &= (other & (0u - other)) - 1u;  // those before the first of another block
+    long long te = tb + 32 - __clz(same);
+    const bool settled = other != 0;
+    bool fresh = __any_sync(FULL, ((same >> lane) & 1u) && row == 0);
+    if (!settled) {
+      for (long long t = tb + 32; t < a.num_tokens; t += 32) {
+        int r;
+        long long p;
+        const int b = append_token<BS, ROPE>(a, t + lane, false, r, p);
+        other = __ballot_sync(FULL, b >= 0 && b != blk);
+        same = __ballot_sync(FULL, b == blk);
+        if (other) same &= (other & (0u - other)) - 1u;
+        if (same) te = t + 32 - __clz(same);
+        fresh |= __any_sync(FULL, ((same >> lane) & 1u) && r == 0);
+        if (other) break;
+      }
     }
-    append_run<E, D, BS, INTERLEAVED, ROPE>(a, is_v, h, ts, te, blk, lane);
+    Window win;
+    if (te - tb <= 32) {  // the first window's tokens are in the lanes
+      const int src = i + lane;
+      const int b = __shfl_sync(FULL, blk_l, src & 31), r = __shfl_sync(FULL, row, src & 31);
+      win.my_pos = __shfl_sync(FULL, pos, src & 31);
+      win.my_row = lane < Window::ROWS && ts + lane < te && b == blk ? r : -1;
+      win.live = __ballot_sync(FULL, win.my_row >= 0);
+    } else {
+      win.tokens(a, ts, te, blk, lane);
+    }
+    for (int hw = hw0; hw < pairs; hw += per) {
+      const bool is_v = hw >= a.num_kv_heads;
+      append_run<E, D, BS, INTERLEAVED, ROPE>(a, win, is_v, is_v ? hw - a.num_kv_heads : hw, ts, te, blk, fresh, lane);
+    }
   }
 }
 
