@@ -128,7 +128,8 @@ int pa_write_kv(const void *k, const void *v, void *k_cache, void *v_cache, cons
  *                  q_out rows become zeros and its K/V are not written.
  *   cos_sin        fp32 [max_positions][rot_dim]: rot_dim / 2 cosines, then
  *                  as many sines, 16-byte aligned.
- *   rot_dim        a positive multiple of 16, at most head_dim.
+ *   rot_dim        a positive multiple of 16, at most head_dim;
+ *                  max_positions at most 2^31 - 1.
  * A negative slot skips the token's K/V only; a slot outside the pool sets
  * PA_DEV_ERR_SLOT and skips them too.  num_tokens == 0 launches nothing.
  */
@@ -177,7 +178,8 @@ int pa_write_kv_fp8(const void *k, const void *v, void *k_cache, void *v_cache, 
 /*
  * pa_rope_write_kv_fp8 -- pa_rope_write_kv into an 8-bit cache: keys are
  * turned in fp32 and quantised from there (one rounding), K and V as
- * pa_write_kv_fp8 stores them, q_out in the storage type.  One launch.
+ * pa_write_kv_fp8 stores them, q_out in the storage type.  One launch for a
+ * decode step, two for long inputs.
  */
 int pa_rope_write_kv_fp8(const void *q, const void *k, const void *v, void *q_out, void *k_cache, void *v_cache,
                          float *k_scale, float *v_scale, const int64_t *slot_mapping, const int64_t *positions,

@@ -2,7 +2,7 @@
 :func:`write_kv`: with the rotary position embedding applied on the way, and into caches held in
 8 bits (e4m3) with one scale for each block and kv head.
 
-Argument marshalling only; the work is one launch of the library's CUDA kernels per call.
+Argument marshalling only; the work is one launch of the library's CUDA kernels per call (two for long inputs into 8 bits).
 8-bit caches are ``torch.float8_e4m3fn`` tensors ``[num_blocks, num_kv_heads, block_size, head_dim]``
 with float32 scales ``[num_blocks, num_kv_heads]``: a stored value stands for value * scale.
 

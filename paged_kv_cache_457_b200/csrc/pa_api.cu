@@ -557,7 +557,7 @@ int check_append(const pa::AppendArgs &a, int head_dim, int dtype, bool rope, bo
   if (a.block_size != 16 && a.block_size != 32) return PA_ERR_UNSUPPORTED;
   if (rope) {
     if (a.rot_dim <= 0 || a.rot_dim > head_dim || a.rot_dim % 16) return PA_ERR_UNSUPPORTED;
-    if (a.max_positions <= 0) return PA_ERR_SHAPE;
+    if (a.max_positions <= 0 || a.max_positions > 0x7fffffffLL) return PA_ERR_SHAPE;
   }
   // head counts whose rows a 32-bit index holds
   if (a.num_q_heads > (1 << 16) || a.num_kv_heads > (1 << 16)) return PA_ERR_SHAPE;
@@ -594,16 +594,28 @@ int finish_launch(cudaError_t e) {
 template <class E, int D>
 int launch_rope_write(const pa::AppendArgs &a, bool interleaved, unsigned grid, cudaStream_t stream) {
   return finish_launch(interleaved
-                           ? launch_pdl(pa::rope_write_kv_kernel<E, D, true>, dim3(grid), dim3(256), 0, stream, a)
-                           : launch_pdl(pa::rope_write_kv_kernel<E, D, false>, dim3(grid), dim3(256), 0, stream, a));
+                           ? launch_pdl(pa::rope_write_kv_kernel<E, D, true>, dim3(grid),
+                                        dim3(pa::ROW_THREADS), 0, stream, a)
+                           : launch_pdl(pa::rope_write_kv_kernel<E, D, false>, dim3(grid),
+                                        dim3(pa::ROW_THREADS), 0, stream, a));
 }
 
 template <class E, int D, int BS>
 int launch_append_fp8(const pa::AppendArgs &a, bool rope, bool interleaved, unsigned grid, cudaStream_t stream) {
-  const dim3 g(grid), b(256);
-  if (!rope) return finish_launch(launch_pdl(pa::append_fp8_kernel<E, D, BS, false, false>, g, b, 0, stream, a));
-  return finish_launch(interleaved ? launch_pdl(pa::append_fp8_kernel<E, D, BS, true, true>, g, b, 0, stream, a)
-                                   : launch_pdl(pa::append_fp8_kernel<E, D, BS, false, true>, g, b, 0, stream, a));
+  auto go = [&](auto kernel) -> int {
+    constexpr uint32_t smem = pa::append_smem(D, BS);
+    if constexpr (smem > 48u * 1024u) {
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return record(e);
+    }
+    return finish_launch(launch_pdl(kernel, dim3(grid), dim3(pa::APPEND_WARPS * 32), smem, stream, a));
+  };
+  if (!rope) return go(pa::append_fp8_kernel<E, D, BS, false, false, false>);
+  if (a.rows > 0)
+    return interleaved ? go(pa::append_fp8_kernel<E, D, BS, true, true, true>)
+                       : go(pa::append_fp8_kernel<E, D, BS, false, true, true>);
+  return interleaved ? go(pa::append_fp8_kernel<E, D, BS, true, true, false>)
+                     : go(pa::append_fp8_kernel<E, D, BS, false, true, false>);
 }
 
 int append_fp8(pa::AppendArgs &a, int head_dim, int dtype, bool rope, bool interleaved, cudaStream_t stream) {
@@ -623,11 +635,26 @@ int append_fp8(pa::AppendArgs &a, int head_dim, int dtype, bool rope, bool inter
          stretches * (pairs / (2 * a.heads_per_warp)) >= (long long)sms * 32)
     a.heads_per_warp *= 2;
   const long long warps = stretches * ((pairs + a.heads_per_warp - 1) / a.heads_per_warp);
-  a.kv_blocks = (warps + 7) / 8;
+  a.kv_blocks = (warps + pa::APPEND_WARPS - 1) / pa::APPEND_WARPS;
+  // The q heads' rows: in the same launch while the call is short (one launch less); long inputs give them one of
+  // their own, since the K/V part's registers leave too few threads on an SM for their loads.
   a.tokens_per_cta = row_tokens_per_cta(a.num_tokens, sms);
-  const long long rows = a.num_q_heads > 0 ? (a.num_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta : 0;
-  if (a.kv_blocks + rows > 0x7fffffffLL) return PA_ERR_SHAPE;
-  const unsigned grid = (unsigned)(a.kv_blocks + rows);
+  const long long row_blocks = a.num_q_heads > 0 ? (a.num_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta : 0;
+  if (a.kv_blocks + row_blocks > 0x7fffffffLL) return PA_ERR_SHAPE;
+  a.rows = a.num_q_heads;
+  long long blocks = a.kv_blocks + row_blocks;
+  if (a.tokens_per_warp > 1 && row_blocks > 0) {
+    auto q_rows = [&](auto e) {
+      using E = decltype(e);
+      return head_dim == 128 ? launch_rope_write<E, 128>(a, interleaved, (unsigned)row_blocks, stream)
+                             : launch_rope_write<E, 64>(a, interleaved, (unsigned)row_blocks, stream);
+    };
+    rc = dtype == PA_BFLOAT16 ? q_rows(pa::BF16{}) : q_rows(pa::F16{});
+    if (rc != PA_OK) return rc;
+    a.rows = 0;
+    blocks = a.kv_blocks;
+  }
+  const unsigned grid = (unsigned)blocks;
   auto go = [&](auto e) {
     using E = decltype(e);
     if (head_dim == 128)
@@ -918,6 +945,7 @@ int pa_rope_write_kv(const void *q, const void *k, const void *v, void *q_out, v
   int sms = 0;
   rc = current_sms(&sms);
   if (rc != PA_OK) return rc;
+  a.rows = num_q_heads + 2 * num_kv_heads;
   a.tokens_per_cta = row_tokens_per_cta(num_tokens, sms);
   const long long grid = (num_tokens + a.tokens_per_cta - 1) / a.tokens_per_cta;
   if (grid > 0x7fffffffLL) return PA_ERR_SHAPE;

@@ -11,13 +11,15 @@
 //
 // rope_write_kv_kernel      16-bit caches: q' out, k' and v to their slots.
 // append_fp8_kernel         8-bit caches: k' and v quantised to their slots,
-//                           q' out in the same launch (later blocks).
+//                           q' out in the same launch (later blocks) for short
+//                           inputs, by rope_write_kv_kernel for long ones.
 //
 // A unit of work of a row is 16 elements: two 16-byte chunks that hold both
 // members of 8 pairs, with their 8 cosines and 8 sines.
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "pa_kernels.cuh"
 
@@ -34,6 +36,7 @@ struct AppendArgs {
   long long q_stride, k_stride, v_stride, q_out_stride;
   long long kv_blocks;        // append_fp8_kernel: grid blocks of the K/V part
   int num_q_heads, num_kv_heads, block_size, rot_dim;
+  int rows;                   // rope_write_kv_kernel: rows of a token it handles (q heads alone, or all)
   int tokens_per_cta;         // row part: consecutive tokens of one block of threads
   int tokens_per_warp;        // append_fp8_kernel: consecutive tokens of one warp (1 or block_size)
   int heads_per_warp;         // append_fp8_kernel: (kv head, K or V) pairs of one warp
@@ -98,35 +101,46 @@ __device__ __forceinline__ Angles load_angles(const AppendArgs &a, long long p, 
   return g;
 }
 
+// Packed fp32 products.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // Turns the unit's 16 elements (chunks lo and hi) in place.
 template <bool INTERLEAVED>
 __device__ __forceinline__ void turn(float (&lo)[8], float (&hi)[8], const Angles &g) {
-  // Scalar products and sums: the packed forms (f32x2) come out contracted into fused ones, whatever their rounding
-  // suffix.
-  auto pair = [&](float &x, float &y, int i) {
-    const float xc = __fmul_rn(x, g.c[i]), ys = __fmul_rn(y, g.s[i]);
-    const float yc = __fmul_rn(y, g.c[i]), xs = __fmul_rn(x, g.s[i]);
-    x = __fsub_rn(xc, ys);
-    y = __fadd_rn(yc, xs);
+  // Pairs i and i + 1 at once: packed products, scalar sums -- a packed product followed by a packed sum is contracted
+  // into a fused one, whatever their rounding suffix.
+  auto two = [&](float &x0, float &y0, float &x1, float &y1, int i) {
+    const float2 x = make_float2(x0, x1), y = make_float2(y0, y1);
+    const float2 c = make_float2(g.c[i], g.c[i + 1]), s = make_float2(g.s[i], g.s[i + 1]);
+    const float2 xc = mul2(x, c), ys = mul2(y, s), yc = mul2(y, c), xs = mul2(x, s);
+    x0 = __fsub_rn(xc.x, ys.x), x1 = __fsub_rn(xc.y, ys.y);
+    y0 = __fadd_rn(yc.x, xs.x), y1 = __fadd_rn(yc.y, xs.y);
   };
   if (INTERLEAVED) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      pair(lo[2 * i], lo[2 * i + 1], i);
-      pair(hi[2 * i], hi[2 * i + 1], 4 + i);
+    for (int i = 0; i < 4; i += 2) {
+      two(lo[2 * i], lo[2 * i + 1], lo[2 * i + 2], lo[2 * i + 3], i);
+      two(hi[2 * i], hi[2 * i + 1], hi[2 * i + 2], hi[2 * i + 3], 4 + i);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) pair(lo[i], hi[i], i);
+    for (int i = 0; i < 8; i += 2) two(lo[i], hi[i], lo[i + 1], hi[i + 1], i);
   }
 }
 
 // ---------------------------------------------------------------- 16-bit rows
-// One item: unit c of rows r0 and r0 + half of token t (rows: q heads, then k heads, then v heads; half =
-// ceil(rows / 2)).  Two rows of a token share the angles and keep four 16-byte loads in flight.  q_out may be q
-// itself: a thread reads the two chunks of a row that it alone writes, before it writes them.
-template <class E, int D, bool INTERLEAVED>
-__device__ __forceinline__ void append_rows(const AppendArgs &a, long long t, int r0, int half, int rows, int c) {
+// One item: unit c of NR rows of token t, r0, r0 + apart, ... (rows: q heads, then k heads, then v heads).  The rows
+// share the angles and keep 2 NR 16-byte loads in flight.  q_out may be q itself: a thread reads the two chunks of a
+// row that it alone writes, before it writes them.
+template <class E, int D, bool INTERLEAVED, int NR>
+__device__ __forceinline__ void append_rows(const AppendArgs &a, long long t, int r0, int apart, int rows, int c) {
   const long long pos = a.positions[t];
   if (pos < 0) return;  // padding: nothing of the token is touched
   const bool pos_ok = pos < a.max_positions;
@@ -140,40 +154,43 @@ __device__ __forceinline__ void append_rows(const AppendArgs &a, long long t, in
   const Unit u = unit_of<INTERLEAVED>(c, a.rot_dim);
   const long long blk = slot_ok ? slot / a.block_size : 0;
   const int row = slot_ok ? (int)(slot - blk * a.block_size) : 0;
-  uint16_t *dst[2] = {nullptr, nullptr};  // of the first chunk; the second lies `apart` elements on
-  int apart[2];
-  bool turned[2];
-  uint4 w[2][2];
+  uint16_t *dst[NR];
+  uint4 w[NR][2];
+  // chunks of row r: a V row keeps its own in order
+  auto chunks = [&](int r) {
+    const bool v = r >= a.num_q_heads + a.num_kv_heads;
+    return make_int2(v ? 2 * c : u.c0, v ? 2 * c + 1 : u.c1);
+  };
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = r0 + i * half;
+  for (int i = 0; i < NR; ++i) {
+    const int r = r0 + i * apart;
     const int hk = r - a.num_q_heads, hv = hk - a.num_kv_heads;
     const uint16_t *src = nullptr;
-    turned[i] = u.rotated && hv < 0;
-    const int c0 = hv < 0 ? u.c0 : 2 * c, c1 = hv < 0 ? u.c1 : 2 * c + 1;  // a V row keeps its chunks in order
-    apart[i] = (c1 - c0) * 8;
+    dst[i] = nullptr;
     if (r < rows) {
       if (hk < 0) {
         src = a.q + t * a.q_stride + (long long)r * D;
-        dst[i] = a.q_out + t * a.q_out_stride + (long long)r * D + c0 * 8;
+        dst[i] = a.q_out + t * a.q_out_stride + (long long)r * D;
       } else if (slot_ok && pos_ok && dcheck(blk < a.num_blocks && row < a.block_size && hv < a.num_kv_heads)) {
         const int h = hv < 0 ? hk : hv;
         src = (hv < 0 ? a.k + t * a.k_stride : a.v + t * a.v_stride) + (long long)h * D;
         dst[i] = static_cast<uint16_t *>(hv < 0 ? a.k_cache : a.v_cache) +
-                 ((blk * a.num_kv_heads + h) * a.block_size + row) * D + c0 * 8;
+                 ((blk * a.num_kv_heads + h) * a.block_size + row) * D;
       }
     }
     if (src) {
-      w[i][0] = *reinterpret_cast<const uint4 *>(src + c0 * 8);
-      w[i][1] = *reinterpret_cast<const uint4 *>(src + c1 * 8);
+      const int2 cc = chunks(r);
+      w[i][0] = *reinterpret_cast<const uint4 *>(src + cc.x * 8);
+      w[i][1] = *reinterpret_cast<const uint4 *>(src + cc.y * 8);
     }
   }
   Angles g;
-  if ((turned[0] || turned[1]) && pos_ok) g = load_angles(a, pos, c);
+  if (u.rotated && pos_ok) g = load_angles(a, pos, c);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < NR; ++i) {
     if (!dst[i]) continue;
-    if (turned[i] && pos_ok) {
+    const int r = r0 + i * apart;
+    if (u.rotated && pos_ok && r < a.num_q_heads + a.num_kv_heads) {
       float lo[8], hi[8];
       E::widen8(w[i][0], lo);
       E::widen8(w[i][1], hi);
@@ -182,8 +199,9 @@ __device__ __forceinline__ void append_rows(const AppendArgs &a, long long t, in
       w[i][1] = narrow8<E>(hi);
     }
     if (!pos_ok) w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);  // only q rows get here: zeros for a bad position
-    *reinterpret_cast<uint4 *>(dst[i]) = w[i][0];
-    *reinterpret_cast<uint4 *>(dst[i] + apart[i]) = w[i][1];
+    const int2 cc = chunks(r);
+    *reinterpret_cast<uint4 *>(dst[i] + cc.x * 8) = w[i][0];
+    *reinterpret_cast<uint4 *>(dst[i] + cc.y * 8) = w[i][1];
   }
 }
 
@@ -191,21 +209,24 @@ __device__ __forceinline__ void append_rows(const AppendArgs &a, long long t, in
 template <class E, int D, bool INTERLEAVED>
 __device__ __forceinline__ void append_row_block(const AppendArgs &a, long long b, int rows) {
   constexpr int UNITS = D / 16;
-  const int half = (rows + 1) / 2;
-  const int per = half * UNITS;
   const long long t0 = b * a.tokens_per_cta;
   const int nt = (int)min((long long)a.tokens_per_cta, a.num_tokens - t0);
+  constexpr int NR = 2;
+  const int apart = (rows + NR - 1) / NR;
+  const int per = apart * UNITS;
   for (int i = threadIdx.x; i < nt * per; i += blockDim.x) {
     const int t = i / per, rem = i - t * per;
-    append_rows<E, D, INTERLEAVED>(a, t0 + t, rem / UNITS, half, rows, rem % UNITS);
+    append_rows<E, D, INTERLEAVED, NR>(a, t0 + t, rem / UNITS, apart, rows, rem % UNITS);
   }
 }
 
+constexpr int ROW_THREADS = 256;
+
 template <class E, int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(256) rope_write_kv_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(ROW_THREADS, 4) rope_write_kv_kernel(const AppendArgs a) {
   grid_dependency_wait();  // the rows may come from the previous kernel in the stream
   grid_launch_dependents();
-  append_row_block<E, D, INTERLEAVED>(a, blockIdx.x, a.num_q_heads + 2 * a.num_kv_heads);
+  append_row_block<E, D, INTERLEAVED>(a, blockIdx.x, a.rows);
 }
 
 // ---------------------------------------------------------------- 8-bit rows
@@ -216,9 +237,10 @@ __global__ void __launch_bounds__(256) rope_write_kv_kernel(const AppendArgs a) 
 //   s_new = pow2_scale(amax) if the run holds the block's row 0 (the block starts anew), else
 //           max(s_old, pow2_scale(amax)); where s_new > s_old the block's bytes become rn(byte * s_old / s_new),
 //   bytes = rn_sat(x' / s_new) to the run's rows.
-// Rows are read in windows of BS tokens and kept in registers (2-byte values) between the two steps; a run is one
-// window unless skipped tokens or a slot named twice stretch it, and only then are rows read twice.  Kept in fp32,
-// rotated, they would save the second rotation but spill (64 registers more).
+// Rows are read in windows of BS tokens by 16-byte asynchronous copies into shared memory, from where each lane reads
+// back what it copied, once for the magnitude and once for the bytes: registers stay free for occupancy, and a
+// warp's next head is on its way while it works on this one.  A run is one window unless skipped tokens or a slot
+// named twice stretch it, and only then are rows fetched twice.
 
 // Token t of the call: its block (-1: not written), row in the block and position.  `flags`: set the status bits.
 template <int BS, bool ROPE>
@@ -240,8 +262,23 @@ __device__ __forceinline__ int append_token(const AppendArgs &a, long long t, bo
 // The largest of |f[i]| and m; NaN counts as nothing.
 __device__ __forceinline__ float amax8(const float (&f)[8], float m) {
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) m = fmaxf(fmaxf(m, fabsf(f[i])), fabsf(f[i + 1]));
+  for (int i = 0; i < 8; i += 2)
+    asm("{\n\t.reg .f32 x, y;\n\tabs.f32 x, %1;\n\tabs.f32 y, %2;\n\tmax.f32 %0, x, y, %3;\n\t}"
+        : "=f"(m)
+        : "f"(f[i]), "f"(f[i + 1]), "f"(m));
   return m;
+}
+
+// 16-byte asynchronous copy global -> shared (zeros when !ok), past L1; a thread's copies and its wait for all but the
+// last N groups of them.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <class E, int D, int BS, bool INTERLEAVED, bool ROPE>
@@ -250,49 +287,52 @@ struct RunWindow {
   static constexpr int RPI = 32 / LPR;  // rows of one pass of the warp
   static constexpr int PASSES = BS / RPI;
   static constexpr int ROWS = BS;
-  uint4 w[PASSES][2];
+  static constexpr uint32_t BYTES = BS * D * 2;  // one buffer: [pass][chunk][lane] pieces of 16 bytes
   int my_row;        // lane i: row of the window's token i in the block, -1: none of the run's
-  long long my_pos;
+  int my_pos;        // its position (below max_positions, at most 2^31 - 1)
   unsigned live;     // lanes with such a row
 
   // Tokens ts .. ts + ROWS - 1 of the run [ts, te) of block blk.
   __device__ __forceinline__ void tokens(const AppendArgs &a, long long ts, long long te, int blk, int lane) {
-    const int b = append_token<BS, ROPE>(a, lane < ROWS && ts + lane < te ? ts + lane : -1, false, my_row, my_pos);
+    long long pos;
+    const int b = append_token<BS, ROPE>(a, lane < ROWS && ts + lane < te ? ts + lane : -1, false, my_row, pos);
+    my_pos = (int)pos;
     if (b != blk) my_row = -1;
     live = __ballot_sync(FULL, my_row >= 0);
   }
-  // The window's rows from `base` (token ts, this head).
-  __device__ __forceinline__ void load(const uint16_t *base, long long stride, const Unit &u, int lane) {
+  // Starts the copies of the window's rows from `base` (token ts, this head) into `buf`, dead rows as zeros.
+  __device__ __forceinline__ void fetch(uint8_t *buf, const uint16_t *base, long long stride, const Unit &u,
+                                        int lane) const {
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-      w[p][0] = w[p][1] = make_uint4(0, 0, 0, 0);
       const int r = p * RPI + lane / LPR;
-      if ((live >> r) & 1u) {
-        const uint16_t *src = base + r * stride;
-        w[p][0] = __ldg(reinterpret_cast<const uint4 *>(src + u.c0 * 8));
-        w[p][1] = __ldg(reinterpret_cast<const uint4 *>(src + u.c1 * 8));
-      }
+      const bool ok = (live >> r) & 1u;
+      const uint16_t *src = ok ? base + r * stride : base;
+      cp_async16(buf + (2 * p) * 512 + lane * 16, src + u.c0 * 8, ok);
+      cp_async16(buf + (2 * p + 1) * 512 + lane * 16, src + u.c1 * 8, ok);
     }
+    cp_async_commit();
   }
   // This lane's 16 values of pass p in fp32, rotated when `turned` (the angles come from L1 the second time).
-  __device__ __forceinline__ void values(const AppendArgs &a, int p, const Unit &u, bool turned, int lane,
-                                         float (&lo)[8], float (&hi)[8]) const {
-    E::widen8(w[p][0], lo);
-    E::widen8(w[p][1], hi);
+  __device__ __forceinline__ void values(const AppendArgs &a, const uint8_t *buf, int p, const Unit &u, bool turned,
+                                         int lane, float (&lo)[8], float (&hi)[8]) const {
+    E::widen8(*reinterpret_cast<const uint4 *>(buf + (2 * p) * 512 + lane * 16), lo);
+    E::widen8(*reinterpret_cast<const uint4 *>(buf + (2 * p + 1) * 512 + lane * 16), hi);
     if (turned) {
       const int r = p * RPI + lane / LPR;
-      const long long pos = __shfl_sync(FULL, my_pos, r);
+      const int pos = __shfl_sync(FULL, my_pos, r);
       if (u.rotated && ((live >> r) & 1u)) turn<INTERLEAVED>(lo, hi, load_angles(a, pos, lane % LPR));
     }
   }
   // Largest finite magnitude of this lane's values.
-  __device__ __forceinline__ float amax(const AppendArgs &a, const Unit &u, bool turned, int lane) const {
+  __device__ __forceinline__ float amax(const AppendArgs &a, const uint8_t *buf, const Unit &u, bool turned,
+                                        int lane) const {
     float m = 0.f;
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       if ((live >> (p * RPI)) == 0) break;
       float lo[8], hi[8];
-      values(a, p, u, turned, lane, lo, hi);
+      values(a, buf, p, u, turned, lane, lo, hi);
       const float all = amax8(hi, amax8(lo, 0.f));
       if (all < INFINITY) {
         m = fmaxf(m, all);
@@ -306,8 +346,8 @@ struct RunWindow {
     }
     return m;
   }
-  __device__ __forceinline__ void store(const AppendArgs &a, uint8_t *slab, const Unit &u, bool turned, float s,
-                                        int lane) const {
+  __device__ __forceinline__ void store(const AppendArgs &a, const uint8_t *buf, uint8_t *slab, const Unit &u,
+                                        bool turned, float s, int lane) const {
     // x / s: by the exact reciprocal where s is a power of two (always, unless the caller's own scale stands)
     const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
     const float inv = __fdiv_rn(1.f, s);
@@ -315,13 +355,14 @@ struct RunWindow {
     for (int p = 0; p < PASSES; ++p) {
       if ((live >> (p * RPI)) == 0) break;
       float lo[8], hi[8];
-      values(a, p, u, turned, lane, lo, hi);
+      values(a, buf, p, u, turned, lane, lo, hi);
       const int row = __shfl_sync(FULL, my_row, p * RPI + lane / LPR);
       if (pow2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          lo[i] = __fmul_rn(lo[i], inv);
-          hi[i] = __fmul_rn(hi[i], inv);
+        for (int i = 0; i < 8; i += 2) {
+          const float2 x = mul2(make_float2(lo[i], lo[i + 1]), make_float2(inv, inv));
+          const float2 y = mul2(make_float2(hi[i], hi[i + 1]), make_float2(inv, inv));
+          lo[i] = x.x, lo[i + 1] = x.y, hi[i] = y.x, hi[i + 1] = y.y;
         }
       } else {
 #pragma unroll
@@ -365,65 +406,53 @@ __device__ __forceinline__ void rescale_slab(uint8_t *slab, float ratio, int lan
   }
 }
 
-// One run for one kv head of K or V.  `win` holds the run's first window of tokens.
-template <class E, int D, int BS, bool INTERLEAVED, bool ROPE>
-__device__ __forceinline__ void append_run(const AppendArgs &a, RunWindow<E, D, BS, INTERLEAVED, ROPE> &win, bool is_v,
-                                           int h, long long ts, long long te, int blk, bool fresh, int lane) {
-  constexpr int ROWS = RunWindow<E, D, BS, INTERLEAVED, ROPE>::ROWS;
-  if (!dcheck(blk >= 0 && blk < a.num_blocks && h < a.num_kv_heads)) return;
-  const bool turned = ROPE && !is_v;
-  const int c = lane % (D / 16);
-  const Unit u = turned ? unit_of<INTERLEAVED>(c, a.rot_dim) : Unit{2 * c, 2 * c + 1, false};
-  const long long stride = is_v ? a.v_stride : a.k_stride;
-  const uint16_t *base = (is_v ? a.v : a.k) + ts * stride + (long long)h * D;
-  const long long head = (long long)blk * a.num_kv_heads + h;
-  float *scale = (is_v ? a.v_scale : a.k_scale) + head;
-  uint8_t *slab = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + head * BS * D;
-  const float s_old = *scale;
-  win.load(base, stride, u, lane);
-  float amax = win.amax(a, u, turned, lane);
-  const bool one = te - ts <= ROWS;
-  if (!one) {
-    for (long long t = ts + ROWS; t < te; t += ROWS) {
-      win.tokens(a, t, te, blk, lane);
-      win.load(base + (t - ts) * stride, stride, u, lane);
-      amax = fmaxf(amax, win.amax(a, u, turned, lane));
-    }
+// One kv head of K or of V of a run that starts at token ts in block blk.
+template <class E, int D, int BS>
+struct RunHead {
+  const uint16_t *base;
+  long long stride;
+  float *scale;
+  uint8_t *slab;
+  Unit u;
+  bool turned;
+  float s_old;
+  template <bool INTERLEAVED, bool ROPE>
+  __device__ __forceinline__ void set(const AppendArgs &a, int hw, long long ts, int blk, int lane) {
+    const bool is_v = hw >= a.num_kv_heads;
+    const int h = is_v ? hw - a.num_kv_heads : hw;
+    const int c = lane % (D / 16);
+    turned = ROPE && !is_v;
+    u = turned ? unit_of<INTERLEAVED>(c, a.rot_dim) : Unit{2 * c, 2 * c + 1, false};
+    stride = is_v ? a.v_stride : a.k_stride;
+    base = (is_v ? a.v : a.k) + ts * stride + (long long)h * D;
+    const long long head = (long long)blk * a.num_kv_heads + h;
+    scale = (is_v ? a.v_scale : a.k_scale) + head;
+    slab = static_cast<uint8_t *>(is_v ? a.v_cache : a.k_cache) + head * BS * D;
+    s_old = *scale;
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, off));
-  const float want = pow2_scale(amax);
-  const float s_new = fresh ? want : fmaxf(s_old, want);
-  if (!fresh && s_new > s_old) {
-    rescale_slab<BS * D>(slab, __fdiv_rn(s_old, s_new), lane);
-    __syncwarp();  // before the run's own rows are written over theirs
-  }
-  if (one) {
-    win.store(a, slab, u, turned, s_new, lane);
-  } else {
-    for (long long t = ts; t < te; t += ROWS) {
-      win.tokens(a, t, te, blk, lane);
-      win.load(base + (t - ts) * stride, stride, u, lane);
-      win.store(a, slab, u, turned, s_new, lane);
-      __syncwarp();
-    }
-    win.tokens(a, ts, te, blk, lane);  // as it was, for the run's next head
-  }
-  if (lane == 0) *scale = s_new;
+};
+
+constexpr int APPEND_WARPS = 4;
+
+// Dynamic shared memory of append_fp8_kernel: two windows per warp.
+__host__ __device__ constexpr uint32_t append_smem(int head_dim, int block_size) {
+  return APPEND_WARPS * 2u * (uint32_t)(block_size * head_dim * 2);
 }
 
 // K/V part: warp w of the part takes tokens [i * tokens_per_warp, +tokens_per_warp) of heads_per_warp (kv head, K or
 // V) pairs, and the runs that START among them (a run's later tokens may lie in the next warps' stretches, which then
-// leave them alone).  Row part (grid blocks from kv_blocks on): the q heads.
-template <class E, int D, int BS, bool INTERLEAVED, bool ROPE>
-__global__ void __launch_bounds__(256, BS * D <= 2048 ? 2 : 1) append_fp8_kernel(const AppendArgs a) {
+// leave them alone).  With Q, grid blocks from kv_blocks on take the q heads' rows: one launch for a decode step.
+template <class E, int D, int BS, bool INTERLEAVED, bool ROPE, bool Q>
+__global__ void __launch_bounds__(APPEND_WARPS * 32, 4) append_fp8_kernel(const AppendArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
-  if (ROPE && (long long)blockIdx.x >= a.kv_blocks) {
+  if (Q && (long long)blockIdx.x >= a.kv_blocks) {
     append_row_block<E, D, INTERLEAVED>(a, (long long)blockIdx.x - a.kv_blocks, a.num_q_heads);
     return;
   }
   using Window = RunWindow<E, D, BS, INTERLEAVED, ROPE>;
+  extern __shared__ __align__(16) uint8_t append_buf[];
+  uint8_t *buf = append_buf + (threadIdx.x >> 5) * 2 * Window::BYTES;
   const int lane = threadIdx.x & 31;
   const long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int pairs = 2 * a.num_kv_heads;
@@ -489,15 +518,64 @@ __global__ void __launch_bounds__(256, BS * D <= 2048 ? 2 : 1) append_fp8_kernel
     if (te - tb <= 32) {  // the first window's tokens are in the lanes
       const int src = i + lane;
       const int b = __shfl_sync(FULL, blk_l, src & 31), r = __shfl_sync(FULL, row, src & 31);
-      win.my_pos = __shfl_sync(FULL, pos, src & 31);
+      win.my_pos = __shfl_sync(FULL, (int)pos, src & 31);
       win.my_row = lane < Window::ROWS && ts + lane < te && b == blk ? r : -1;
       win.live = __ballot_sync(FULL, win.my_row >= 0);
     } else {
       win.tokens(a, ts, te, blk, lane);
     }
+    if (!dcheck(blk < a.num_blocks)) continue;
+    const bool one = te - ts <= Window::ROWS;
+    RunHead<E, D, BS> cur, next;
+    cur.template set<INTERLEAVED, ROPE>(a, hw0, ts, blk, lane);
+    win.fetch(buf, cur.base, cur.stride, cur.u, lane);
+    int at = 0;  // buffer of the current head
     for (int hw = hw0; hw < pairs; hw += per) {
-      const bool is_v = hw >= a.num_kv_heads;
-      append_run<E, D, BS, INTERLEAVED, ROPE>(a, win, is_v, is_v ? hw - a.num_kv_heads : hw, ts, te, blk, fresh, lane);
+      uint8_t *b = buf + at * Window::BYTES;
+      const bool more = one && hw + per < pairs;
+      if (more) {  // the next head's rows, while this one is worked on
+        next.template set<INTERLEAVED, ROPE>(a, hw + per, ts, blk, lane);
+        win.fetch(buf + (at ^ 1) * Window::BYTES, next.base, next.stride, next.u, lane);
+        cp_async_wait<1>();
+      } else {
+        cp_async_wait<0>();
+      }
+      float amax = win.amax(a, b, cur.u, cur.turned, lane);
+      if (!one) {
+        for (long long t = ts + Window::ROWS; t < te; t += Window::ROWS) {
+          win.tokens(a, t, te, blk, lane);
+          win.fetch(b, cur.base + (t - ts) * cur.stride, cur.stride, cur.u, lane);
+          cp_async_wait<0>();
+          amax = fmaxf(amax, win.amax(a, b, cur.u, cur.turned, lane));
+        }
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, off));
+      const float want = pow2_scale(amax);
+      const float s_new = fresh ? want : fmaxf(cur.s_old, want);
+      if (!fresh && s_new > cur.s_old) {
+        rescale_slab<BS * D>(cur.slab, __fdiv_rn(cur.s_old, s_new), lane);
+        __syncwarp();  // before the run's own rows are written over theirs
+      }
+      if (one) {
+        win.store(a, b, cur.slab, cur.u, cur.turned, s_new, lane);
+      } else {
+        for (long long t = ts; t < te; t += Window::ROWS) {
+          win.tokens(a, t, te, blk, lane);
+          win.fetch(b, cur.base + (t - ts) * cur.stride, cur.stride, cur.u, lane);
+          cp_async_wait<0>();
+          win.store(a, b, cur.slab, cur.u, cur.turned, s_new, lane);
+          __syncwarp();
+        }
+        win.tokens(a, ts, te, blk, lane);
+        if (hw + per < pairs) {
+          next.template set<INTERLEAVED, ROPE>(a, hw + per, ts, blk, lane);
+          win.fetch(b, next.base, next.stride, next.u, lane);
+        }
+      }
+      if (lane == 0) *cur.scale = s_new;
+      cur = next;
+      if (one) at ^= 1;
     }
   }
 }
