@@ -679,7 +679,7 @@ int append_fp8(pa::AppendArgs &a, int head_dim, int dtype, bool rope, bool inter
 #define PA_BLOCKS8 3
 #endif
 #ifndef PA_TAIL_CHUNKS8
-#define PA_TAIL_CHUNKS8 1
+#define PA_TAIL_CHUNKS8 2
 #endif
 constexpr int kWarps8 = PA_WARPS8, kStages8 = PA_STAGES8, kBlocks8 = PA_BLOCKS8;
 static_assert(kWarps8 == kWarps, "blocks_per_sm sizes blocks with kWarps warps");

@@ -12,8 +12,9 @@
 //     maximum of zv, p_j = 2^(zv_j - m + 7) is the weight that multiplies the
 //     bytes, and l += p_j / sv(j) the normaliser, so that out = acc / l and the
 //     weights stay in fp16's range whatever the scales are.  p is rounded to
-//     fp16 (half a step: 2^-11 of it; l adds the rounded values where they are
-//     normal, so weights still sum to one) -- the bytes carry 2^-4.  Factor 2^7: weights down to
+//     fp16 (half a step: 2^-11 of it; l adds the rounded values, a product of
+//     P with a row of ones, so weights still sum to one) -- the bytes carry
+//     2^-4.  Factor 2^7: weights down to
 //     2^-31 of the largest are kept, and the largest, 2^(7 + RESCALE_SLACK),
 //     fits.
 // A query row in bf16 is scaled by a power of two to magnitudes in
@@ -124,7 +125,10 @@ struct Math8 {
   static constexpr int KSTEPS = D / 16;
   uint32_t qb[KSTEPS][2];
   float o[KSTEPS][4];  // [16 dims][dim 2 gid: head a, head b; dim 2 gid + 1: head a, head b]
-  float ma, mb, la, lb, qa, qbs;  // per head column a = 2 tig, b = 2 tig + 1; qa, qbs: score scales (base-2 units)
+  // per head column a = 2 tig, b = 2 tig + 1: the running maximum of zv less 7 (the weights' exponent offset), the
+  // normaliser over all lanes, and the score scales (base-2 units)
+  float ma, mb, la, lb, qa, qbs;
+  float lv_top;  // largest log2 of a V scale so far in the piece
 
   // Query rows qrow + g * D of heads g < G.
   __device__ __forceinline__ void begin(const uint16_t *qrow, int G, bool ok, float scale_log2, int lane) {
@@ -171,17 +175,13 @@ struct Math8 {
     qbs = __shfl_sync(FULL, unit, 8 * tig + 4) * scale_log2;  // head 2 tig + 1
 #pragma unroll
     for (int c = 0; c < KSTEPS; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
-    ma = mb = -INFINITY;
+    ma = mb = lv_top = -INFINITY;
     la = lb = 0.f;
   }
 
-  // What a weight adds to l: its rounded value, unless fp16 has lost bits of it.  Under a tiny scale (a block of
-  // zeros among others) p is tiny while p / sv is not.
-  static __device__ __forceinline__ float summed(float rounded, float p) { return rounded >= 6.103515625e-5f ? rounded : p; }
-
   // One tile at kt, vt (shared-memory addresses) with its scales (K of tokens 0-15 and 16-31, V likewise); nvalid live
   // rows.  The caller has made sure that the slot's bytes have arrived; it is free again when this returns.
-  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, const float4 sc4, int nvalid, int lane) {
+  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, float4 sc4, int nvalid, int lane) {
     const int gid = lane >> 2, tig = lane & 3;
     float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     constexpr int CH = D / 64;  // 16-byte chunks of a row per lane
@@ -203,29 +203,53 @@ struct Math8 {
           mma_16816_f16(sc[mt], af, qb[4 * i + j][0], qb[4 * i + j][1]);
         }
     }
-    // a scale of zero (a block of zeros) would send the exponent to -inf: its bytes are zeros, any small scale will do
-    const float v0 = fmaxf(sc4.z, 5.421011e-20f), v1 = fmaxf(sc4.w, 5.421011e-20f);
-    const float lv[2] = {lg2(v0), lg2(v1)};
-    const float ks[2] = {sc4.x, sc4.y};
-    float z[2][4];
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const bool lo = mt * 16 + gid < nvalid, hi = mt * 16 + 8 + gid < nvalid;
-      z[mt][0] = lo ? fmaf(sc[mt][0], ks[mt] * qa, lv[mt]) : -INFINITY;
-      z[mt][1] = lo ? fmaf(sc[mt][1], ks[mt] * qbs, lv[mt]) : -INFINITY;
-      z[mt][2] = hi ? fmaf(sc[mt][2], ks[mt] * qa, lv[mt]) : -INFINITY;
-      z[mt][3] = hi ? fmaf(sc[mt][3], ks[mt] * qbs, lv[mt]) : -INFINITY;
+    if (nvalid < TILE8) {
+      if (nvalid <= 16) {  // a half without rows has no scales of its own
+        sc4.y = sc4.x;
+        sc4.w = sc4.z;
+      }
+      clear_tail(vt, nvalid, lane);
     }
-    float ca = fmaxf(fmaxf(z[0][0], z[0][2]), fmaxf(z[1][0], z[1][2]));
-    float cb = fmaxf(fmaxf(z[0][1], z[0][3]), fmaxf(z[1][1], z[1][3]));
-    if (__any_sync(FULL, ca > ma + RESCALE_SLACK || cb > mb + RESCALE_SLACK)) {
+    // a scale of zero (a block of zeros) would send the exponent to -inf: its bytes are zeros, any small scale will do
+    const float lv[2] = {lg2(fmaxf(sc4.z, 5.421011e-20f)), lg2(fmaxf(sc4.w, 5.421011e-20f))};
+    const float ka[2] = {sc4.x * qa, sc4.y * qa}, kb[2] = {sc4.x * qbs, sc4.y * qbs};
+    // exponents of the weights, e = z + lv - (m - 7); dead rows -inf
+    float e[2][4];
+    auto exponents = [&]() {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const float ca = lv[mt] - ma, cb = lv[mt] - mb;
+        e[mt][0] = fmaf(sc[mt][0], ka[mt], ca);
+        e[mt][1] = fmaf(sc[mt][1], kb[mt], cb);
+        e[mt][2] = fmaf(sc[mt][2], ka[mt], ca);
+        e[mt][3] = fmaf(sc[mt][3], kb[mt], cb);
+      }
+      if (nvalid < TILE8) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          if (mt * 16 + gid >= nvalid) e[mt][0] = e[mt][1] = -INFINITY;
+          if (mt * 16 + 8 + gid >= nvalid) e[mt][2] = e[mt][3] = -INFINITY;
+        }
+      }
+    };
+    exponents();
+    // raise m only when some weight passes 2^(7 + slack): on the piece's first tile (m = -inf) and seldom after it
+    const float top = fmaxf(fmax3(fmaxf(e[0][0], e[0][1]), e[0][2], e[0][3]),
+                            fmax3(fmaxf(e[1][0], e[1][1]), e[1][2], e[1][3]));
+    if (__any_sync(FULL, top > 7.f + RESCALE_SLACK)) {
+      const float oa = ma, ob = mb;
+      ma = mb = 0.f;
+      exponents();  // z + lv themselves
+      float ca = fmaxf(fmaxf(e[0][0], e[0][2]), fmaxf(e[1][0], e[1][2]));
+      float cb = fmaxf(fmaxf(e[0][1], e[0][3]), fmaxf(e[1][1], e[1][3]));
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         ca = fmaxf(ca, __shfl_xor_sync(FULL, ca, off));
         cb = fmaxf(cb, __shfl_xor_sync(FULL, cb, off));
       }
-      const float na = fmaxf(ma, ca), nb = fmaxf(mb, cb);
-      const float fa = ex2(ma - na), fb = ex2(mb - nb);  // 0 on the piece's first tile
+      ma = fmaxf(oa, ca - 7.f);
+      mb = fmaxf(ob, cb - 7.f);
+      const float fa = ex2(oa - ma), fb = ex2(ob - mb);  // 0 on the piece's first tile
 #pragma unroll
       for (int c = 0; c < KSTEPS; ++c) {
         o[c][0] *= fa;
@@ -235,33 +259,33 @@ struct Math8 {
       }
       la *= fa;
       lb *= fb;
-      ma = na;
-      mb = nb;
+      exponents();
     }
+    lv_top = fmax3(lv_top, lv[0], lv[1]);
     uint32_t pb[2][2];
-    const float iv[2] = {__frcp_rn(v0), __frcp_rn(v1)};
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      if (mt * 16 >= nvalid) {  // the half may never have been copied: neither its bytes nor its scales count
-        pb[mt][0] = pb[mt][1] = 0u;
-        continue;
-      }
-      const float e0 = ex2(z[mt][0] - ma + 7.f), e1 = ex2(z[mt][1] - mb + 7.f);
-      const float e2 = ex2(z[mt][2] - ma + 7.f), e3 = ex2(z[mt][3] - mb + 7.f);
-      const uint32_t h01 = F16::narrow2(e0, e1), h23 = F16::narrow2(e2, e3);
-      const float2 p01 = __half22float2(*reinterpret_cast<const __half2 *>(&h01));
-      const float2 p23 = __half22float2(*reinterpret_cast<const __half2 *>(&h23));
-      la = fmaf(summed(p01.x, e0) + summed(p23.x, e2), iv[mt], la);
-      lb = fmaf(summed(p01.y, e1) + summed(p23.y, e3), iv[mt], lb);
-      pb[mt][0] = movmatrix_trans(h01);
-      pb[mt][1] = movmatrix_trans(h23);
-    }
-    // masks of this lane's token pairs (2 tig, 2 tig + 1) + 8 i: bytes past the sequence may be NaN, and 0 * NaN is not 0
-    uint32_t keep[4];
+      const float p0 = ex2(e[mt][0]), p1 = ex2(e[mt][1]), p2 = ex2(e[mt][2]), p3 = ex2(e[mt][3]);
+      pb[mt][0] = movmatrix_trans(F16::narrow2(p0, p1));
+      pb[mt][1] = movmatrix_trans(F16::narrow2(p2, p3));
+      // l: P times ones (every row of the product holds the sums of the rounded weights)
+      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+      mma_16816_f16(ls, ones, pb[mt][0], pb[mt][1]);
+      float sa = ls[0], sb = ls[1];
+      if (lv[mt] < lv_top - 10.f) {  // uniform, rare: under a scale this small fp16 has lost weights that count in l
+        sa = p0 + p2;
+        sb = p1 + p3;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      keep[i] = (8 * i + 2 * tig < nvalid ? 0x0000ffffu : 0u) | (8 * i + 2 * tig + 1 < nvalid ? 0xffff0000u : 0u);
-    const bool partial = nvalid < TILE8;
+        for (int off = 4; off < 32; off <<= 1) {
+          sa += __shfl_xor_sync(FULL, sa, off);
+          sb += __shfl_xor_sync(FULL, sb, off);
+        }
+      }
+      const float iv = ex2(-lv[mt]);
+      la = fmaf(sa, iv, la);
+      lb = fmaf(sb, iv, lb);
+    }
 #pragma unroll
     for (int c = 0; c < KSTEPS; ++c) {
       uint32_t r[4];
@@ -272,10 +296,6 @@ struct Math8 {
         const uint32_t x = __byte_perm(r[i], 0, 0x3120);  // (dim 2 gid of both tokens, dim 2 gid + 1 of both)
         lo[i] = e4m3x2_to_f16x2((uint16_t)x);
         hi[i] = e4m3x2_to_f16x2((uint16_t)(x >> 16));
-        if (partial) {
-          lo[i] &= keep[i];
-          hi[i] &= keep[i];
-        }
       }
       const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
       mma_16816_f16(o[c], a0, pb[0][0], pb[0][1]);
@@ -283,13 +303,12 @@ struct Math8 {
     }
   }
 
-  // Totals of l over the lanes of a head column.
-  __device__ __forceinline__ void totals() {
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      la += __shfl_xor_sync(FULL, la, off);
-      lb += __shfl_xor_sync(FULL, lb, off);
-    }
+  // V's rows from nvalid on become zeros in place: they may hold NaN, or bytes never copied, and 0 * NaN is not 0.
+  static __device__ __noinline__ void clear_tail(uint32_t vt, int nvalid, int lane) {
+    for (int i = nvalid * D + lane * 4; i < TILE8 * D; i += 128)
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(vt + i), "r"(0) : "memory");  // whole rows: the swizzle permutes within one
+    fence_proxy_async_smem();
+    __syncwarp();
   }
 };
 
@@ -341,7 +360,8 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   bool prod_done = false;
   TilePos cp = locate_tile(pt, S, HC, plan.start(cons_c));
   TilePos pos = cp;  // the producer's next tile
-  int win_s = -1, win_base = 0, ent = -1, prod_L = 0;
+  int win_s = -1, win_base = 0, ent = -1, prod_L = 0, prod_hc = -1, prod_h = 0;
+  const unsigned nblocks = (unsigned)a.num_blocks;  // below 2^31, as are the rows (checked on the host)
   uint32_t bad_slots = 0;
   uint32_t iter = 0, issued = 0;
 
@@ -361,14 +381,14 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       pos = locate_tile(pt, S, HC, plan.start(nc));
     }
     const int st = (int)(issued++ % STAGES);
-    const int b0 = pos.j * TILE8 / a.block_size;
+    const int b0 = two ? 2 * pos.j : pos.j;
     if (pos.s != win_s || b0 < win_base || b0 >= win_base + 32) {
       // a window of 32 entries of the row; those past the sequence's last tile are not read, and the one past its last
       // block (an odd count of 16-token blocks) is never used
       if (pos.s != win_s) prod_L = __ldg(a.context_lens + pos.s);
       win_s = pos.s;
       win_base = b0 & ~31;
-      const int n = min(a.table_stride, pos.nt * TILE8 / a.block_size);
+      const int n = min(a.table_stride, two ? 2 * pos.nt : pos.nt);
       ent = (win_base + lane < n && dcheck(pos.s < S))
                 ? __ldg(a.block_tables + (long long)pos.s * a.table_stride + win_base + lane)
                 : -1;
@@ -376,26 +396,35 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     const int p0 = __shfl_sync(FULL, ent, b0 - win_base);
     const int p1 = two ? __shfl_sync(FULL, ent, (b0 + 1 - win_base) & 31) : p0;  // b0 is even: the same window
     const bool second = two && pos.j * TILE8 + 16 < prod_L;
-    const int h = pos.hc / a.n_chunks;
-    const bool good = p0 >= 0 && (long long)p0 < a.num_blocks &&
-                      (!second || (p1 >= 0 && (long long)p1 < a.num_blocks)) && dcheck(h < a.num_kv_heads);
+    if (pos.hc != prod_hc) {
+      prod_hc = pos.hc;
+      prod_h = pos.hc / a.n_chunks;
+    }
+    if (pos.j == 0) {  // a new segment: its query rows on their way to L1, where the consumer will ask for them
+      const int g = lane >> 2;
+      if (g < G)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + (long long)pos.s * a.q_seq_stride +
+                                                       (long long)(chunk_first_head(a, pos.hc) + g) * D + (lane & 3) * (D / 4)));
+    }
+    const int h = prod_h;
+    const bool good = (unsigned)p0 < nblocks && (!second || (unsigned)p1 < nblocks) && dcheck(h < a.num_kv_heads);
     bad_slots = good ? (bad_slots & ~(1u << st)) : (bad_slots | (1u << st));
     if (lane < 4) {
       if (good && (!(lane & 1) || second || !two))
-        cp_async4(scales + st * 4 + lane, ((lane & 2) ? args.v_scale : args.k_scale) +
-                                              (long long)((lane & 1) ? p1 : p0) * a.num_kv_heads + h);
+        cp_async4(scales + st * 4 + lane,
+                  ((lane & 2) ? args.v_scale : args.k_scale) + (((lane & 1) ? p1 : p0) * a.num_kv_heads + h));
       cp_async_arrive(&bars[st]);
     }
     if (lane == 0) {
       fence_proxy_async_smem();
       if (good) {
         unsigned char *kd = ring + st * Smem::STAGE_BYTES, *vd = kd + Smem::TILE_BYTES;
-        const int r0 = (int)(((long long)p0 * a.num_kv_heads + h) * a.block_size);
+        const int r0 = (p0 * a.num_kv_heads + h) * a.block_size;
         mbar_arrive_expect_tx(&bars[st], (second || !two) ? Smem::STAGE_BYTES : Smem::STAGE_BYTES / 2);
         tma_load_2d(kd, &tmap_k, 0, r0, &bars[st]);
         tma_load_2d(vd, &tmap_v, 0, r0, &bars[st]);
         if (second) {
-          const int r1 = (int)(((long long)p1 * a.num_kv_heads + h) * a.block_size);
+          const int r1 = (p1 * a.num_kv_heads + h) * a.block_size;
           tma_load_2d(kd + Smem::TILE_BYTES / 2, &tmap_k, 0, r1, &bars[st]);
           tma_load_2d(vd + Smem::TILE_BYTES / 2, &tmap_v, 0, r1, &bars[st]);
         }
@@ -448,7 +477,6 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     ++iter;
 
     if (cp.j + 1 == cp.nt || cons_left == 1) {  // end of the piece
-      cm.totals();
       if (piece_bad && lane == 0) atomicOr(&g_status, PA_DEV_ERR_BLOCK_ID);
       const int gid = lane >> 2, ha = 2 * (lane & 3), hb = ha + 1;
       if (full) {
