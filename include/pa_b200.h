@@ -509,8 +509,8 @@ int pa_decode_cascade(const void *q, const void *k_cache, const void *v_cache, c
  * past its last block, may hold anything.  num_blocks * num_kv_heads *
  * block_size must not exceed 2^31 - 1 (PA_ERR_SHAPE).  Caches are 16-byte
  * aligned, scales 4-byte.
- * The workspace (pa_decode_fp8_workspace_size bytes, 16-byte aligned) is
- * scratch of one call in flight at a time.
+ * The workspace (pa_decode_fp8_workspace_size bytes, 16-byte aligned; small
+ * calls need none) is scratch of one call in flight at a time.
  */
 size_t pa_decode_fp8_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                     int32_t block_size, int32_t max_context_len, int32_t partition_tokens);
@@ -525,12 +525,14 @@ int pa_decode_fp8(const void *q, const void *k_cache, const void *v_cache, const
  * pa_prefill_fp8 -- pa_prefill over an 8-bit cache whose rows of the new
  * tokens are already written (pa_write_kv_fp8, pa_rope_write_kv_fp8).
  * Arguments, layouts and device-side errors as pa_prefill, except that a
- * needed table entry outside the pool zeroes the (256 new tokens, head) items
- * that need it.  K and V are widened and scaled to the storage type of q
+ * table entry outside the pool zeroes at least the rows that need it and at
+ * most those of the same sequence, and that rows past max_query_len may or
+ * may not be written.  K and V are widened and scaled to the storage type of q
  * (exact where the scale is a power of two and the value a normal number of
  * that type, saturating at fp16's largest value otherwise), products and sums
- * are fp32, softmax weights are rounded to the storage type.  Any finite
- * `scale`.  A NaN among the values of a sequence's live tokens may reach all
+ * are fp32, softmax weights are rounded to the storage type.  Calls of few new
+ * tokens per sequence (max_query_len up to 16) run on pa_decode_fp8's kernels
+ * and arithmetic instead.  Any finite `scale`.  A NaN among the values of a sequence's live tokens may reach all
  * of its rows in the call.
  *   workspace   device scratch of pa_prefill_fp8_workspace_size bytes,
  *               16-byte aligned; needs no initialisation.  Calls that may run

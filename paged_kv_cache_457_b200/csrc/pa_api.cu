@@ -678,9 +678,6 @@ int append_fp8(pa::AppendArgs &a, int head_dim, int dtype, bool rope, bool inter
 #ifndef PA_BLOCKS8
 #define PA_BLOCKS8 3
 #endif
-#ifndef PA_TAIL_CHUNKS8
-#define PA_TAIL_CHUNKS8 2
-#endif
 constexpr int kWarps8 = PA_WARPS8, kStages8 = PA_STAGES8, kBlocks8 = PA_BLOCKS8;
 static_assert(kWarps8 == kWarps, "blocks_per_sm sizes blocks with kWarps warps");
 
@@ -692,49 +689,80 @@ int heads_per_unit8(int group) {
   return 1;
 }
 
-template <class E, int D>
+template <class E, int D, bool FEW>
 const void *split8_kernel() {
-  return reinterpret_cast<const void *>(pa::decode8_split_kernel<E, D, kWarps8, kStages8, kBlocks8>);
+  return reinterpret_cast<const void *>(pa::decode8_split_kernel<E, D, kWarps8, kStages8, kBlocks8, FEW>);
 }
+template <bool FEW>
 const void *split8_kernel_for(int dtype, int head_dim) {
-  if (dtype == PA_BFLOAT16) return head_dim == 128 ? split8_kernel<pa::BF16, 128>() : split8_kernel<pa::BF16, 64>();
-  return head_dim == 128 ? split8_kernel<pa::F16, 128>() : split8_kernel<pa::F16, 64>();
+  if (dtype == PA_BFLOAT16)
+    return head_dim == 128 ? split8_kernel<pa::BF16, 128, FEW>() : split8_kernel<pa::BF16, 64, FEW>();
+  return head_dim == 128 ? split8_kernel<pa::F16, 128, FEW>() : split8_kernel<pa::F16, 64, FEW>();
 }
 uint32_t split8_smem(int head_dim, int num_seqs) {
   return head_dim == 128 ? pa::Smem8<128, kWarps8, kStages8>::bytes(num_seqs)
                          : pa::Smem8<64, kWarps8, kStages8>::bytes(num_seqs);
 }
 
-// As plan_decode, on tiles of pa::TILE8 tokens.
-int plan_decode8(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len,
+template <class E, int D, bool FEW>
+const void *segment8_kernel() {
+  return reinterpret_cast<const void *>(pa::decode8_segment_kernel<E, D, kWarps8, FEW>);
+}
+template <bool FEW>
+const void *segment8_kernel_for(int dtype, int head_dim) {
+  if (dtype == PA_BFLOAT16)
+    return head_dim == 128 ? segment8_kernel<pa::BF16, 128, FEW>() : segment8_kernel<pa::BF16, 64, FEW>();
+  return head_dim == 128 ? segment8_kernel<pa::F16, 128, FEW>() : segment8_kernel<pa::F16, 64, FEW>();
+}
+uint32_t segment8_smem(int head_dim) {
+  return head_dim == 128 ? pa::SegSmem8<128, kWarps8>::BYTES : pa::SegSmem8<64, kWarps8>::BYTES;
+}
+// Units of at most this many tiles may take the per-unit kernel (kWarps8 warps x 4).
+#ifndef PA_SEG8_TILES
+#define PA_SEG8_TILES 64
+#endif
+constexpr int kSegmentMaxTiles8 = PA_SEG8_TILES;
+
+// As plan_decode, on tiles of pa::TILE8 tokens; num_groups row groups of `columns` columns per unit, HC units each.
+template <bool FEW>
+int plan_decode8(long long num_groups, int columns, int HC, int head_dim, long long max_context_len,
                  int partition_tokens, int dtype, LaunchPlan *lp) {
   if (partition_tokens < 0 || partition_tokens % pa::TILE != 0) return PA_ERR_PARTITION;
   int sms = 0;
   int rc = current_sms(&sms);
   if (rc != PA_OK) return rc;
-  const int group = num_q_heads / num_kv_heads;
-  const int G = heads_per_unit8(group);
+  const long long max_tiles = (max_context_len + pa::TILE8 - 1) / pa::TILE8;
   lp->segment_mode = false;
-  lp->smem = split8_smem(head_dim, num_seqs);
+  if (partition_tokens == 0 && max_tiles <= kSegmentMaxTiles8) {
+    lp->smem = segment8_smem(head_dim);
+    int o16 = 0, o_bf = 0;
+    if ((rc = blocks_per_sm(segment8_kernel_for<FEW>(PA_FLOAT16, head_dim), lp->smem, &o16)) != PA_OK) return rc;
+    if ((rc = blocks_per_sm(segment8_kernel_for<FEW>(PA_BFLOAT16, head_dim), lp->smem, &o_bf)) != PA_OK) return rc;
+    if (num_groups * HC <= (long long)sms * std::min(o16, o_bf)) {
+      lp->segment_mode = true;
+      lp->grid = (int)(num_groups * HC);
+      lp->chunk_tiles = 0;
+      lp->max_chunks = 0;
+      lp->queue_bytes = lp->tiles_bytes = lp->ml_bytes = lp->acc_bytes = lp->total_bytes = 0;
+      return PA_OK;
+    }
+  }
+  lp->smem = split8_smem(head_dim, (int)num_groups);
   if (lp->smem > 227u * 1024u) return PA_ERR_SHAPE;
   int occ_f16 = 0, occ_bf16 = 0;
-  if ((rc = blocks_per_sm(split8_kernel_for(PA_FLOAT16, head_dim), lp->smem, &occ_f16)) != PA_OK) return rc;
-  if ((rc = blocks_per_sm(split8_kernel_for(PA_BFLOAT16, head_dim), lp->smem, &occ_bf16)) != PA_OK) return rc;
+  if ((rc = blocks_per_sm(split8_kernel_for<FEW>(PA_FLOAT16, head_dim), lp->smem, &occ_f16)) != PA_OK) return rc;
+  if ((rc = blocks_per_sm(split8_kernel_for<FEW>(PA_BFLOAT16, head_dim), lp->smem, &occ_bf16)) != PA_OK) return rc;
   const long long ws_warps = (long long)sms * std::max(occ_f16, occ_bf16) * kWarps8;
   lp->grid = dtype == 0 ? 0 : sms * (dtype == PA_BFLOAT16 ? occ_bf16 : occ_f16);
   lp->chunk_tiles = (partition_tokens + pa::TILE8 - 1) / pa::TILE8;
-  if (lp->chunk_tiles == 0) {
-    lp->max_chunks = ws_warps * (1 + PA_TAIL_CHUNKS8) + 1;
-  } else {
-    const long long per_seq = ((long long)max_context_len + pa::TILE8 - 1) / pa::TILE8;
-    const long long total = (long long)num_seqs * num_kv_heads * (group / G) * per_seq;
-    lp->max_chunks = std::max(1LL, (total + lp->chunk_tiles - 1) / lp->chunk_tiles);
-  }
+  if (lp->chunk_tiles == 0)
+    lp->max_chunks = ws_warps * (1 + pa::TAIL8_MOST) + 1;
+  else
+    lp->max_chunks = std::max(1LL, (num_groups * HC * max_tiles + lp->chunk_tiles - 1) / lp->chunk_tiles);
   lp->queue_bytes = 256;
-  lp->tiles_bytes = (((size_t)num_seqs + 1) * sizeof(int) + 255) / 256 * 256;
-  lp->ml_bytes = (size_t)lp->max_chunks * 2 * G * sizeof(float2);
-  lp->ml_bytes = (lp->ml_bytes + 255) / 256 * 256;
-  lp->acc_bytes = (size_t)lp->max_chunks * 2 * G * head_dim * sizeof(float);
+  lp->tiles_bytes = (((size_t)num_groups + 1) * sizeof(int) + 255) / 256 * 256;
+  lp->ml_bytes = ((size_t)lp->max_chunks * 2 * columns * sizeof(float2) + 255) / 256 * 256;
+  lp->acc_bytes = (size_t)lp->max_chunks * 2 * columns * head_dim * sizeof(float);
   lp->total_bytes = lp->queue_bytes + lp->tiles_bytes + lp->ml_bytes + lp->acc_bytes;
   return PA_OK;
 }
@@ -760,18 +788,79 @@ int fp8_tensor_map(const void *base, long long rows, int head_dim, int block_siz
   return PA_OK;
 }
 
-template <class E, int D>
+template <class E, int D, bool FEW>
 int launch_decode8(const pa::Decode8Args &a, const LaunchPlan &lp, const CUtensorMap &mk, const CUtensorMap &mv,
                    cudaStream_t stream) {
-  int rc = finish_launch(launch_pdl(pa::decode8_split_kernel<E, D, kWarps8, kStages8, kBlocks8>, dim3(lp.grid),
-                                    dim3(kWarps8 * 32), lp.smem, stream, mk, mv, a));
+  const dim3 block(kWarps8 * 32);
+  if (lp.segment_mode)
+    return finish_launch(launch_pdl(pa::decode8_segment_kernel<E, D, kWarps8, FEW>, dim3(lp.grid), block, lp.smem, stream, a));
+  int rc = finish_launch(launch_pdl(pa::decode8_split_kernel<E, D, kWarps8, kStages8, kBlocks8, FEW>, dim3(lp.grid), block,
+                                    lp.smem, stream, mk, mv, a));
   if (rc != PA_OK) return rc;
-  // one warp per two heads of a segment (one for an odd number of heads), as after decode_split_mma_kernel
-  const int hw = a.d.heads_per_unit % 2 == 0 ? 2 : 1;
-  const long long warps = (long long)a.d.num_seqs * a.d.num_kv_heads * a.d.n_chunks * (a.d.heads_per_unit / hw);
-  const dim3 grid((unsigned)((warps + 7) / 8)), block(256);
-  return finish_launch(hw == 2 ? launch_pdl(pa::decode_merge_kernel<E, D, 2, 4>, grid, block, 0, stream, a.d)
-                               : launch_pdl(pa::decode_merge_kernel<E, D, 1, 4>, grid, block, 0, stream, a.d));
+  // one warp per two columns of a unit (one for an odd number), as after decode_split_mma_kernel
+  const int columns = a.tokens * a.d.heads_per_unit, hw = columns % 2 == 0 ? 2 : 1;
+  const long long warps = (long long)a.d.num_seqs * a.d.num_kv_heads * a.d.n_chunks * (columns / hw);
+  const dim3 grid((unsigned)((warps + 7) / 8)), mblock(256);
+  return finish_launch(hw == 2 ? launch_pdl(pa::decode8_merge_kernel<E, D, 2, 4, FEW>, grid, mblock, 0, stream, a)
+                               : launch_pdl(pa::decode8_merge_kernel<E, D, 1, 4, FEW>, grid, mblock, 0, stream, a));
+}
+
+// Fills what follows from the sizes and the plan, and launches.  `a` holds the pointers, strides, row groups,
+// max_context_len and scale.
+template <bool FEW>
+int run_decode8(pa::Decode8Args &args, const LaunchPlan &lp, int head_dim, int dtype, void *workspace,
+                cudaStream_t stream) {
+  pa::DecodeArgs &a = args.d;
+  char *ws = static_cast<char *>(workspace);
+  if (!lp.segment_mode) {
+    a.ws_queue = reinterpret_cast<unsigned long long *>(ws);
+    a.ws_tiles = reinterpret_cast<int *>(ws + lp.queue_bytes);
+    a.ws_ml = reinterpret_cast<float2 *>(ws + lp.queue_bytes + lp.tiles_bytes);
+    a.ws_acc = reinterpret_cast<float *>(ws + lp.queue_bytes + lp.tiles_bytes + lp.ml_bytes);
+  }
+  a.max_chunks = lp.max_chunks;
+  a.wait_limit_ns = kWaitLimitNs;
+  a.group = a.num_q_heads / a.num_kv_heads;
+  a.heads_per_unit = heads_per_unit8(a.group);
+  a.n_chunks = a.group / a.heads_per_unit;
+  a.chunk_tiles = lp.chunk_tiles;
+  a.split_warps = lp.grid * kWarps8;
+  a.epoch = next_epoch();
+  CUtensorMap mk{}, mv{};
+  if (!lp.segment_mode) {
+    const long long rows = a.num_blocks * a.num_kv_heads * a.block_size;
+    int rc = fp8_tensor_map(args.k_cache, rows, head_dim, a.block_size, &mk);
+    if (rc != PA_OK) return rc;
+    rc = fp8_tensor_map(args.v_cache, rows, head_dim, a.block_size, &mv);
+    if (rc != PA_OK) return rc;
+  }
+  if (dtype == PA_BFLOAT16)
+    return head_dim == 128 ? launch_decode8<pa::BF16, 128, FEW>(args, lp, mk, mv, stream)
+                           : launch_decode8<pa::BF16, 64, FEW>(args, lp, mk, mv, stream);
+  return head_dim == 128 ? launch_decode8<pa::F16, 128, FEW>(args, lp, mk, mv, stream)
+                         : launch_decode8<pa::F16, 64, FEW>(args, lp, mk, mv, stream);
+}
+
+// A prefill call of few tokens per sequence runs on the decode kernels, a row group per tokens that fill the eight
+// columns; more go to the 128-row tiles of prefill8_tc_kernel.
+#ifndef PA_FEW_TOKENS8
+#define PA_FEW_TOKENS8 16
+#endif
+struct FewTokens {
+  bool use;
+  int tokens, groups, columns, HC;
+  long long num_groups;
+};
+FewTokens few_tokens(int num_seqs, int num_q_heads, int num_kv_heads, int max_query_len) {
+  FewTokens f{};
+  const int group = num_q_heads / num_kv_heads, G = heads_per_unit8(group);
+  f.tokens = std::max(1, std::min(8 / G, max_query_len));
+  f.groups = (max_query_len + f.tokens - 1) / f.tokens;
+  f.columns = f.tokens * G;
+  f.HC = num_kv_heads * (group / G);
+  f.num_groups = (long long)num_seqs * f.groups;
+  f.use = max_query_len <= PA_FEW_TOKENS8 && f.num_groups <= 4096;
+  return f;
 }
 
 // Block copies of 8-bit pools: blocks and the scales of their heads, in one launch.
@@ -834,7 +923,8 @@ size_t pa_decode_fp8_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32
   if (check_decode_shape(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len) != PA_OK)
     return 0;
   LaunchPlan lp;
-  if (plan_decode8(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, partition_tokens, 0, &lp) != PA_OK)
+  const int G = heads_per_unit8(num_q_heads / num_kv_heads);
+  if (plan_decode8<false>(num_seqs, G, num_q_heads / G, head_dim, max_context_len, partition_tokens, 0, &lp) != PA_OK)
     return 0;
   return lp.total_bytes;
 }
@@ -863,31 +953,20 @@ int pa_decode_fp8(const void *q, const void *k_cache, const void *v_cache, const
        reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens)) & 3u)
     return PA_ERR_ALIGN;
   LaunchPlan lp;
-  rc = plan_decode8(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, partition_tokens, dtype, &lp);
+  const int G = heads_per_unit8(num_q_heads / num_kv_heads);
+  rc = plan_decode8<false>(num_seqs, G, num_q_heads / G, head_dim, max_context_len, partition_tokens, dtype, &lp);
   if (rc != PA_OK) return rc;
-  if (!workspace || workspace_bytes < lp.total_bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
-  CUtensorMap mk, mv;
-  const long long rows = num_blocks * num_kv_heads * block_size;
-  if ((rc = fp8_tensor_map(k_cache, rows, head_dim, block_size, &mk)) != PA_OK) return rc;
-  if ((rc = fp8_tensor_map(v_cache, rows, head_dim, block_size, &mv)) != PA_OK) return rc;
-
-  const int group = num_q_heads / num_kv_heads;
-  char *ws = static_cast<char *>(workspace);
+  if (lp.total_bytes > 0 && (!workspace || workspace_bytes < lp.total_bytes || !aligned16(workspace)))
+    return PA_ERR_WORKSPACE;
   pa::Decode8Args args{};
   pa::DecodeArgs &a = args.d;
   a.q = static_cast<const uint16_t *>(q);
   a.block_tables = block_tables;
   a.context_lens = context_lens;
   a.out = static_cast<uint16_t *>(out);
-  a.ws_queue = reinterpret_cast<unsigned long long *>(ws);
-  a.ws_tiles = reinterpret_cast<int *>(ws + lp.queue_bytes);
-  a.ws_ml = reinterpret_cast<float2 *>(ws + lp.queue_bytes + lp.tiles_bytes);
-  a.ws_acc = reinterpret_cast<float *>(ws + lp.queue_bytes + lp.tiles_bytes + lp.ml_bytes);
   a.num_blocks = num_blocks;
   a.q_seq_stride = q_seq_stride;
   a.out_seq_stride = out_seq_stride;
-  a.max_chunks = lp.max_chunks;
-  a.wait_limit_ns = kWaitLimitNs;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);  // log2(e)
   a.num_seqs = num_seqs;
   a.num_q_heads = num_q_heads;
@@ -895,22 +974,12 @@ int pa_decode_fp8(const void *q, const void *k_cache, const void *v_cache, const
   a.block_size = block_size;
   a.table_stride = block_table_stride;
   a.max_context_len = max_context_len;
-  a.group = group;
-  a.heads_per_unit = heads_per_unit8(group);
-  a.n_chunks = group / a.heads_per_unit;
-  a.chunk_tiles = lp.chunk_tiles;
-  a.split_warps = lp.grid * kWarps8;
-  a.static_permille = 0;
-  a.tail_chunks_per_warp = PA_TAIL_CHUNKS8;
-  a.epoch = next_epoch();
+  args.k_cache = static_cast<const uint8_t *>(k_cache);
+  args.v_cache = static_cast<const uint8_t *>(v_cache);
   args.k_scale = k_scale;
   args.v_scale = v_scale;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == PA_BFLOAT16)
-    return head_dim == 128 ? launch_decode8<pa::BF16, 128>(args, lp, mk, mv, st)
-                           : launch_decode8<pa::BF16, 64>(args, lp, mk, mv, st);
-  return head_dim == 128 ? launch_decode8<pa::F16, 128>(args, lp, mk, mv, st)
-                         : launch_decode8<pa::F16, 64>(args, lp, mk, mv, st);
+  args.tokens = args.groups = 1;
+  return run_decode8<false>(args, lp, head_dim, dtype, workspace, static_cast<cudaStream_t>(stream));
 }
 
 int pa_rope_write_kv(const void *q, const void *k, const void *v, void *q_out, void *k_cache, void *v_cache,
@@ -1460,7 +1529,11 @@ size_t pa_prefill_fp8_workspace_size(int32_t num_seqs, int64_t num_query_tokens,
   if (check_prefill8_shape(num_seqs, num_query_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
                            max_query_len) != PA_OK)
     return 0;
-  return 256;  // the work counter
+  const FewTokens f = few_tokens(num_seqs, num_q_heads, num_kv_heads, max_query_len);
+  if (!f.use || f.num_groups == 0) return 256;  // the work counter
+  LaunchPlan lp;  // of the split kernel: whether the per-unit kernel will do depends on the table's width too
+  if (plan_decode8<true>(f.num_groups, f.columns, f.HC, head_dim, 0x7fffffff, 0, 0, &lp) != PA_OK) return 0;
+  return lp.total_bytes;
 }
 
 int pa_prefill_fp8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
@@ -1487,7 +1560,41 @@ int pa_prefill_fp8(const void *q, const void *k_cache, const void *v_cache, cons
        reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(query_start) |
        reinterpret_cast<uintptr_t>(context_lens)) & 3u)
     return PA_ERR_ALIGN;
-  if (num_blocks == 0) return PA_ERR_SHAPE;
+  if (num_blocks == 0 || num_blocks > 0x7fffffffLL / ((long long)num_kv_heads * block_size)) return PA_ERR_SHAPE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const FewTokens f = few_tokens(num_seqs, num_q_heads, num_kv_heads, max_query_len);
+  if (f.use && block_table_stride > 0) {
+    LaunchPlan lp;
+    rc = plan_decode8<true>(f.num_groups, f.columns, f.HC, head_dim, (long long)block_table_stride * block_size, 0, dtype, &lp);
+    if (rc != PA_OK) return rc;
+    if (lp.total_bytes > 0 && (!workspace || workspace_bytes < lp.total_bytes || !aligned16(workspace)))
+      return PA_ERR_WORKSPACE;
+    pa::Decode8Args args{};
+    pa::DecodeArgs &a = args.d;
+    a.q = static_cast<const uint16_t *>(q);
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.out = static_cast<uint16_t *>(out);
+    a.num_blocks = num_blocks;
+    a.q_seq_stride = q_token_stride;
+    a.out_seq_stride = out_token_stride;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634);  // log2(e)
+    a.num_seqs = (int)f.num_groups;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.block_size = block_size;
+    a.table_stride = block_table_stride;
+    a.max_context_len = 0x7fffffff;
+    args.k_cache = static_cast<const uint8_t *>(k_cache);
+    args.v_cache = static_cast<const uint8_t *>(v_cache);
+    args.k_scale = k_scale;
+    args.v_scale = v_scale;
+    args.query_start = query_start;
+    args.num_query_tokens = num_query_tokens;
+    args.tokens = f.tokens;
+    args.groups = f.groups;
+    return run_decode8<true>(args, lp, head_dim, dtype, workspace, st);
+  }
   if (!workspace || workspace_bytes < 256 || !aligned16(workspace)) return PA_ERR_WORKSPACE;
   auto encode = tensor_map_encoder(&rc);
   if (!encode) return rc;
@@ -1536,7 +1643,6 @@ int pa_prefill_fp8(const void *q, const void *k_cache, const void *v_cache, cons
   rc = current_sms(&sms);
   if (rc != PA_OK) return rc;
   const dim3 grid((unsigned)std::min<long long>(a.num_items, sms));  // persistent: one CTA fills an SM
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t me = cudaMemsetAsync(a.queue, 0, sizeof(unsigned int), st);
   if (me != cudaSuccess) return record(me);
   auto launch = [&](auto kernel, uint32_t smem) -> int {

@@ -21,8 +21,12 @@
 // [2^14, 2^15) and so becomes fp16 without loss (elements below 2^-28 of the
 // row's largest excepted); the power is undone with the score's scale.
 //
-// Per warp and tile of 32 tokens (G <= 8 query heads as the 8 columns):
+// Per warp and tile of 32 tokens, 8 columns (below):
 //   S^T[32 x 8] = K[32 x d] Q^T,  O^T[d x 8] += V^T[d x 32] P^T[32 x 8].
+// The columns are the query heads that share the kv head, G at a time, of one
+// token, or of several consecutive new tokens of a sequence (P tokens, P G <=
+// 8) when a call brings a few per sequence: a K/V tile is then read and
+// widened once for all of them, and a column's mask ends at its own token.
 // The contraction over head dims may run in any order as long as K and Q agree:
 // lane tig of a row takes d / 4 consecutive bytes, so K fragments are plain
 // 16-byte shared-memory loads.  V^T needs pairs of tokens side by side:
@@ -42,22 +46,102 @@ namespace pa {
 constexpr int TILE8 = 32;  // tokens per tile of the 8-bit kernels
 
 struct Decode8Args {
-  DecodeArgs d;  // k_cache / v_cache unused (tensor maps); chunk_tiles counts tiles of TILE8 tokens
+  // d.num_seqs counts row groups; d.q_seq_stride and d.out_seq_stride step from token to token; d.chunk_tiles counts
+  // tiles of TILE8 tokens; d.k_cache and d.v_cache are unused
+  DecodeArgs d;
+  const uint8_t *k_cache, *v_cache;
   const float *k_scale, *v_scale;
+  // FEW kernels: [sequences + 1] first query token of each sequence
+  const int32_t *query_start;
+  long long num_query_tokens;
+  int tokens;  // P: query tokens of a row group
+  int groups;  // row groups of a sequence (1 for decode)
 };
 
-__device__ __forceinline__ int seq_tiles8(const DecodeArgs &a, int L) {
-  return (context_ok(a, L) && L > 0) ? (L + TILE8 - 1) / TILE8 : 0;
+// Row group v: up to P consecutive query tokens of a sequence, attended together.
+struct RowGroup {
+  int s;    // sequence (table row)
+  int L;    // tokens of the context that the group's last token sees; below 1: its rows are zeros
+  int tok;  // first query token
+  int cnt;  // query tokens, 0: none
+};
+
+// FEW: row groups of several tokens per sequence (query_start); else one token per sequence (decode), and what several
+// would take folds away.
+template <bool FEW>
+__device__ __forceinline__ RowGroup row_group(const Decode8Args &a, int v) {
+  RowGroup g;
+  if constexpr (!FEW) {
+    const int L = __ldg(a.d.context_lens + v);
+    g.s = g.tok = v;
+    g.cnt = 1;
+    g.L = context_ok(a.d, L) ? L : -1;
+    return g;
+  }
+  g.s = v / a.groups;
+  const int i0 = (v - g.s * a.groups) * a.tokens;
+  const int q0 = __ldg(a.query_start + g.s), n = __ldg(a.query_start + g.s + 1) - q0;
+  const int ctx = __ldg(a.d.context_lens + g.s);
+  const bool rows_ok = q0 >= 0 && n >= 0 && (long long)q0 + n <= a.num_query_tokens;
+  g.tok = q0 + i0;
+  g.cnt = rows_ok ? max(0, min(a.tokens, n - i0)) : 0;
+  g.L = ctx >= n && (long long)ctx <= (long long)a.d.table_stride * a.d.block_size ? ctx - n + i0 + g.cnt : -1;
+  return g;
+}
+// Status bits of the inputs behind row group v, reported once per sequence.
+template <bool FEW>
+__device__ __forceinline__ unsigned row_group_errors(const Decode8Args &a, int v) {
+  if constexpr (!FEW) {
+    const int L = __ldg(a.d.context_lens + v);
+    if (context_ok(a.d, L)) return 0;
+    return (L < 0 || (long long)L > (long long)a.d.table_stride * a.d.block_size) ? PA_DEV_ERR_CONTEXT
+                                                                                  : PA_DEV_ERR_CONTEXT_HINT;
+  }
+  const int s = v / a.groups;
+  if (v != s * a.groups) return 0;
+  const int q0 = __ldg(a.query_start + s), n = __ldg(a.query_start + s + 1) - q0;
+  if (q0 < 0 || n < 0 || (long long)q0 + n > a.num_query_tokens) return PA_DEV_ERR_CONTEXT;
+  const unsigned hint = n > a.groups * a.tokens ? PA_DEV_ERR_CONTEXT_HINT : 0;
+  return hint | (n > 0 && row_group<FEW>(a, v).L < 0 ? PA_DEV_ERR_CONTEXT : 0);
+}
+__device__ __forceinline__ int group_tiles(const RowGroup &g) {
+  return g.cnt > 0 && g.L > 0 ? (g.L + TILE8 - 1) / TILE8 : 0;
 }
 
-// pt[s] = tiles (per head chunk) of the sequences before s; all threads of the block, ends with a barrier.
-__device__ __forceinline__ void build_tile_prefix8(const DecodeArgs &a, int *pt, int *scratch) {
-  const int S = a.num_seqs, nth = blockDim.x, tid = threadIdx.x;
+// The cut of the tile stream (see ChunkPlan): uniform chunks, `tail` of them per warp on average.  Long streams take
+// several, so that warps that run ahead take over from those that lag (8 contexts of 16k-32k tokens: 278, 268, 265 and
+// 264 us with 1, 2, 3 and 5); short ones one, since each cut leaves pieces to merge (256 sequences of 32 q / 8 kv
+// heads, 31 tiles per warp: 104, 105, 107 and 109 us).
+constexpr int TAIL8_TILES = 16, TAIL8_MOST = 3, MIN_CHUNK8_TILES = 2;
+__device__ __forceinline__ ChunkPlan plan_chunks8(const DecodeArgs &a, int tiles_per_head_chunk_set) {
+  ChunkPlan p;
+  p.total = (long long)tiles_per_head_chunk_set * a.num_kv_heads * a.n_chunks;
+  const long long W = a.split_warps;
+  auto ceil_div = [](long long x, long long y) {
+    return x < 0x7fffffffLL && y < 0x7fffffffLL ? (long long)(((unsigned)x + (unsigned)y - 1u) / (unsigned)y)
+                                                 : (x + y - 1) / y;
+  };
+  long long c = a.chunk_tiles;
+  if (c == 0) {
+    const long long tail = max(1LL, min((long long)TAIL8_MOST, p.total / (W * TAIL8_TILES)));
+    c = max((long long)MIN_CHUNK8_TILES, ceil_div(p.total, W * tail));
+  }
+  c = max(c, ceil_div(p.total, a.max_chunks));  // never more chunks than the workspace holds
+  p.c1 = p.c2 = max(c, 1LL);
+  p.count = ceil_div(p.total, p.c1);
+  p.n1 = min(W, p.count);
+  return p;
+}
+
+// pt[v] = tiles (per head chunk) of the row groups before v; all threads of the block, ends with a barrier.
+template <bool FEW>
+__device__ __forceinline__ void build_tile_prefix8(const Decode8Args &a, int *pt, int *scratch) {
+  const int S = a.d.num_seqs, nth = blockDim.x, tid = threadIdx.x;
   const int per = (S + nth - 1) / nth;
   const int i0 = min(S, tid * per), i1 = min(S, i0 + per);
   int sum = 0;
   for (int i = i0; i < i1; ++i) {
-    const int nt = seq_tiles8(a, __ldg(a.context_lens + i));
+    const int nt = group_tiles(row_group<FEW>(a, i));
     pt[i + 1] = nt;
     sum += nt;
   }
@@ -119,23 +203,42 @@ struct Smem8 {
 };
 constexpr int BAR8_ARRIVALS = 1 + 4;  // lane 0's (with the tile's bytes) and one per scale
 
-// The arithmetic of one piece (a run of tiles of one head chunk of G <= 8 query heads), one warp.
-template <class E, int D>
+// The columns of a lane: its query row's (column gid) and its accumulators' (a = 2 tig, b = 2 tig + 1).  Column c is
+// query head c % G of the unit and token c / G of the row group.
+template <bool FEW>
+struct Columns {
+  int G, gid, tig;
+  __device__ __forceinline__ Columns(int G_, int lane) : G(G_), gid(lane >> 2), tig(lane & 3) {}
+  __device__ __forceinline__ int tok(int c) const { return FEW ? c / G : (c >= G ? 1 : 0); }
+  // Elements from the row group's first row to column c's row of query head hq0 + ..., rows `stride` apart.
+  template <int D>
+  __device__ __forceinline__ long long offset(int c, int hq0, long long stride) const {
+    const int t = FEW ? c / G : 0;
+    return t * stride + (long long)(hq0 + c - t * G) * D;
+  }
+};
+
+// The arithmetic of one piece (a run of tiles of one unit: a row group and a head chunk), one warp.
+template <class E, int D, bool FEW>
 struct Math8 {
   static constexpr int KSTEPS = D / 16;
   uint32_t qb[KSTEPS][2];
-  float o[KSTEPS][4];  // [16 dims][dim 2 gid: head a, head b; dim 2 gid + 1: head a, head b]
-  // per head column a = 2 tig, b = 2 tig + 1: the running maximum of zv less 7 (the weights' exponent offset), the
-  // normaliser over all lanes, and the score scales (base-2 units)
+  float o[KSTEPS][4];  // [16 dims][dim 2 gid: column a, b; dim 2 gid + 1: column a, b]
+  // per column a, b: the running maximum of zv less 7 (the weights' exponent offset), the normaliser over all lanes,
+  // and the score scales (base-2 units)
   float ma, mb, la, lb, qa, qbs;
-  float lv_top;  // largest log2 of a V scale so far in the piece
+  float lv_top;     // largest log2 of a V scale so far in the piece
+  int La, Lb, least;  // FEW: context tokens that columns a and b see, and the fewest that any column sees
 
-  // Query rows qrow + g * D of heads g < G.
-  __device__ __forceinline__ void begin(const uint16_t *qrow, int G, bool ok, float scale_log2, int lane) {
-    const int gid = lane >> 2, tig = lane & 3;
-    const bool live = ok && gid < G;
+  // The query rows of group g, unit's first head hq0.
+  __device__ __forceinline__ void begin(const Decode8Args &args, const RowGroup &g, int hq0, bool ok,
+                                        const Columns<FEW> &col) {
+    const DecodeArgs &a = args.d;
+    const bool live = ok && col.tok(col.gid) < g.cnt;
     uint4 w[D / 32];
-    const uint4 *src = reinterpret_cast<const uint4 *>(qrow + (long long)(live ? gid : 0) * D + tig * (D / 4));
+    const uint4 *src = reinterpret_cast<const uint4 *>(
+        a.q + (live ? (long long)g.tok * a.q_seq_stride + col.offset<D>(col.gid, hq0, a.q_seq_stride) : 0) +
+        col.tig * (D / 4));
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) w[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
     float unit = 1.f;
@@ -171,17 +274,25 @@ struct Math8 {
         qb[2 * i + 1][1] = w[i].w;
       }
     }
-    qa = __shfl_sync(FULL, unit, 8 * tig) * scale_log2;       // lane of head 2 tig, any of its four
-    qbs = __shfl_sync(FULL, unit, 8 * tig + 4) * scale_log2;  // head 2 tig + 1
+    qa = __shfl_sync(FULL, unit, 8 * col.tig) * a.scale_log2;       // a lane of column 2 tig
+    qbs = __shfl_sync(FULL, unit, 8 * col.tig + 4) * a.scale_log2;  // column 2 tig + 1
 #pragma unroll
     for (int c = 0; c < KSTEPS; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
     ma = mb = lv_top = -INFINITY;
     la = lb = 0.f;
+    if constexpr (FEW) {
+      least = g.L - (g.cnt - 1);
+      La = min(g.L, least + col.tok(2 * col.tig));
+      Lb = min(g.L, least + col.tok(2 * col.tig + 1));
+    }
   }
 
   // One tile at kt, vt (shared-memory addresses) with its scales (K of tokens 0-15 and 16-31, V likewise); nvalid live
-  // rows.  The caller has made sure that the slot's bytes have arrived; it is free again when this returns.
-  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, float4 sc4, int nvalid, int lane) {
+  // rows, tokens j0 and on.  The caller has made sure that the slot's bytes have arrived; it is free again when this
+  // returns.
+  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, float4 sc4, int nvalid, int j0, int lane) {
+    // live rows that columns a and b see, and the fewest that any column sees
+    const int na = FEW ? La - j0 : nvalid, nb = FEW ? Lb - j0 : nvalid, fewest = FEW ? least - j0 : nvalid;
     const int gid = lane >> 2, tig = lane & 3;
     float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     constexpr int CH = D / 64;  // 16-byte chunks of a row per lane
@@ -224,11 +335,13 @@ struct Math8 {
         e[mt][2] = fmaf(sc[mt][2], ka[mt], ca);
         e[mt][3] = fmaf(sc[mt][3], kb[mt], cb);
       }
-      if (nvalid < TILE8) {
+      if (fewest < TILE8) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          if (mt * 16 + gid >= nvalid) e[mt][0] = e[mt][1] = -INFINITY;
-          if (mt * 16 + 8 + gid >= nvalid) e[mt][2] = e[mt][3] = -INFINITY;
+          if (mt * 16 + gid >= na) e[mt][0] = -INFINITY;
+          if (mt * 16 + gid >= nb) e[mt][1] = -INFINITY;
+          if (mt * 16 + 8 + gid >= na) e[mt][2] = -INFINITY;
+          if (mt * 16 + 8 + gid >= nb) e[mt][3] = -INFINITY;
         }
       }
     };
@@ -249,7 +362,8 @@ struct Math8 {
       }
       ma = fmaxf(oa, ca - 7.f);
       mb = fmaxf(ob, cb - 7.f);
-      const float fa = ex2(oa - ma), fb = ex2(ob - mb);  // 0 on the piece's first tile
+      // 0 on the piece's first tile; a column that has seen no key yet has nothing to scale
+      const float fa = ma > -INFINITY ? ex2(oa - ma) : 0.f, fb = mb > -INFINITY ? ex2(ob - mb) : 0.f;
 #pragma unroll
       for (int c = 0; c < KSTEPS; ++c) {
         o[c][0] *= fa;
@@ -303,6 +417,23 @@ struct Math8 {
     }
   }
 
+  // The normalised rows of group g (zeros when bad).
+  __device__ __forceinline__ void store_output(const Decode8Args &args, const RowGroup &g, int hq0, bool bad,
+                                               const Columns<FEW> &col) const {
+    const DecodeArgs &a = args.d;
+    const float ia = 1.f / la, ib = 1.f / lb;
+    uint16_t *rows = a.out + (long long)g.tok * a.out_seq_stride;
+    uint16_t *ra = rows + col.offset<D>(2 * col.tig, hq0, a.out_seq_stride);
+    uint16_t *rb = rows + col.offset<D>(2 * col.tig + 1, hq0, a.out_seq_stride);
+    const bool wa = col.tok(2 * col.tig) < g.cnt, wb = col.tok(2 * col.tig + 1) < g.cnt;
+#pragma unroll
+    for (int c = 0; c < KSTEPS; ++c) {
+      const int d = 16 * c + 2 * col.gid;
+      if (wa) *reinterpret_cast<uint32_t *>(ra + d) = bad ? 0u : E::narrow2(o[c][0] * ia, o[c][2] * ia);
+      if (wb) *reinterpret_cast<uint32_t *>(rb + d) = bad ? 0u : E::narrow2(o[c][1] * ib, o[c][3] * ib);
+    }
+  }
+
   // V's rows from nvalid on become zeros in place: they may hold NaN, or bytes never copied, and 0 * NaN is not 0.
   static __device__ __noinline__ void clear_tail(uint32_t vt, int nvalid, int lane) {
     for (int i = nvalid * D + lane * 4; i < TILE8 * D; i += 128)
@@ -312,10 +443,35 @@ struct Math8 {
   }
 };
 
+// The physical blocks of a unit's tiles, through a 32-entry window of the table row (one entry per lane).  Entries past
+// the row group's last tile are not read, and the one past its last block (an odd count of 16-token blocks) is never
+// used.
+struct TileLookup {
+  int win_s = -1, win_base = 0, ent = -1;
+  // Tile j of row `s` (nt tiles): *p0 the block of its first 16 tokens, *p1 that of the other 16 (second: whether there
+  // are such).  Returns whether the blocks lie in the pool.
+  __device__ __forceinline__ bool find(const DecodeArgs &a, int s, int nt, int j, int L, int lane, int *p0, int *p1,
+                                       bool *second) {
+    const bool two = a.block_size == 16;
+    const int b0 = two ? 2 * j : j;
+    if (s != win_s || b0 < win_base || b0 >= win_base + 32) {
+      win_s = s;
+      win_base = b0 & ~31;
+      const int n = min(a.table_stride, two ? 2 * nt : nt);
+      ent = win_base + lane < n ? __ldg(a.block_tables + (long long)s * a.table_stride + win_base + lane) : -1;
+    }
+    const unsigned nblocks = (unsigned)a.num_blocks;  // below 2^31, as are the rows (checked on the host)
+    *p0 = __shfl_sync(FULL, ent, b0 - win_base);
+    *p1 = two ? __shfl_sync(FULL, ent, (b0 + 1 - win_base) & 31) : *p0;  // b0 is even: the same window
+    *second = two && j * TILE8 + 16 < L;
+    return (unsigned)*p0 < nblocks && (!*second || (unsigned)*p1 < nblocks);
+  }
+};
+
 // Decode split kernel: the work decomposition of decode_split_mma_kernel (a balanced stream of tiles cut into chunks,
-// pieces merged by decode_merge_kernel) on tiles of 32 tokens; K and V tiles arrive by TMA, the tile's scales by
-// 4-byte asynchronous copies that complete on the same barrier.
-template <class E, int D, int WARPS, int STAGES, int BLOCKS>
+// pieces merged by a second kernel) on tiles of 32 tokens and units of a row group and a head chunk; K and V tiles
+// arrive by TMA, the tile's scales by 4-byte asynchronous copies that complete on the same barrier.
+template <class E, int D, int WARPS, int STAGES, int BLOCKS, bool FEW>
 __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     decode8_split_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                          const Decode8Args args) {
@@ -342,13 +498,13 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   grid_launch_dependents();  // the merge kernel may launch now and wait for this grid
   if (blockIdx.x == 0 && threadIdx.x == 0) atomicExch(a.ws_queue, (unsigned long long)a.epoch << 32);
   const int S = a.num_seqs;
-  build_tile_prefix8(a, pt, pt + S + 1);
+  build_tile_prefix8<FEW>(args, pt, pt + S + 1);
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= S; i += blockDim.x) a.ws_tiles[i] = pt[i];
-  const ChunkPlan plan = plan_chunks(a, pt[S]);
+  const ChunkPlan plan = plan_chunks8(a, pt[S]);
   const int HC = a.num_kv_heads * a.n_chunks;
-  const int G = a.heads_per_unit;
-  const bool two = a.block_size == 16;  // a tile spans two blocks
+  const Columns<FEW> col(a.heads_per_unit, lane);
+  const int C = FEW ? args.tokens * a.heads_per_unit : a.heads_per_unit;  // columns in use
 
   long long cons_c = (long long)blockIdx.x * WARPS + warp;  // chunk the consumer is in (the first one is static)
   if (cons_c >= plan.count) return;
@@ -360,8 +516,9 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   bool prod_done = false;
   TilePos cp = locate_tile(pt, S, HC, plan.start(cons_c));
   TilePos pos = cp;  // the producer's next tile
-  int win_s = -1, win_base = 0, ent = -1, prod_L = 0, prod_hc = -1, prod_h = 0;
-  const unsigned nblocks = (unsigned)a.num_blocks;  // below 2^31, as are the rows (checked on the host)
+  TileLookup look;
+  int prod_v = -1, prod_hc = -1, prod_h = 0;
+  int prod_row = 0, prod_L = 0;  // table row and context of the producer's row group
   uint32_t bad_slots = 0;
   uint32_t iter = 0, issued = 0;
 
@@ -381,36 +538,33 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       pos = locate_tile(pt, S, HC, plan.start(nc));
     }
     const int st = (int)(issued++ % STAGES);
-    const int b0 = two ? 2 * pos.j : pos.j;
-    if (pos.s != win_s || b0 < win_base || b0 >= win_base + 32) {
-      // a window of 32 entries of the row; those past the sequence's last tile are not read, and the one past its last
-      // block (an odd count of 16-token blocks) is never used
-      if (pos.s != win_s) prod_L = __ldg(a.context_lens + pos.s);
-      win_s = pos.s;
-      win_base = b0 & ~31;
-      const int n = min(a.table_stride, two ? 2 * pos.nt : pos.nt);
-      ent = (win_base + lane < n && dcheck(pos.s < S))
-                ? __ldg(a.block_tables + (long long)pos.s * a.table_stride + win_base + lane)
-                : -1;
+    if (pos.s != prod_v) {
+      prod_v = pos.s;
+      const RowGroup pg = row_group<FEW>(args, pos.s);
+      prod_row = pg.s;
+      prod_L = pg.L;
     }
-    const int p0 = __shfl_sync(FULL, ent, b0 - win_base);
-    const int p1 = two ? __shfl_sync(FULL, ent, (b0 + 1 - win_base) & 31) : p0;  // b0 is even: the same window
-    const bool second = two && pos.j * TILE8 + 16 < prod_L;
     if (pos.hc != prod_hc) {
       prod_hc = pos.hc;
       prod_h = pos.hc / a.n_chunks;
     }
-    if (pos.j == 0) {  // a new segment: its query rows on their way to L1, where the consumer will ask for them
-      const int g = lane >> 2;
-      if (g < G)
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + (long long)pos.s * a.q_seq_stride +
-                                                       (long long)(chunk_first_head(a, pos.hc) + g) * D + (lane & 3) * (D / 4)));
-    }
     const int h = prod_h;
-    const bool good = (unsigned)p0 < nblocks && (!second || (unsigned)p1 < nblocks) && dcheck(h < a.num_kv_heads);
+    // a new segment: its query rows on their way to L1, where the consumer will ask for them
+    if (pos.j == 0) {
+      const RowGroup pg = row_group<FEW>(args, pos.s);
+      if (col.tok(col.gid) < pg.cnt)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + (long long)pg.tok * a.q_seq_stride +
+                                                       col.offset<D>(col.gid, chunk_first_head(a, pos.hc), a.q_seq_stride) +
+                                                       col.tig * (D / 4)));
+    }
+    int p0, p1;
+    bool second;
+    const bool found = look.find(a, prod_row, pos.nt, pos.j, prod_L, lane, &p0, &p1, &second);
+    const bool good = found && dcheck(h < a.num_kv_heads && pos.j * TILE8 < prod_L);
+    const bool whole = second || a.block_size != 16;  // both halves are copied
     bad_slots = good ? (bad_slots & ~(1u << st)) : (bad_slots | (1u << st));
     if (lane < 4) {
-      if (good && (!(lane & 1) || second || !two))
+      if (good && (!(lane & 1) || whole))
         cp_async4(scales + st * 4 + lane,
                   ((lane & 2) ? args.v_scale : args.k_scale) + (((lane & 1) ? p1 : p0) * a.num_kv_heads + h));
       cp_async_arrive(&bars[st]);
@@ -420,7 +574,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       if (good) {
         unsigned char *kd = ring + st * Smem::STAGE_BYTES, *vd = kd + Smem::TILE_BYTES;
         const int r0 = (p0 * a.num_kv_heads + h) * a.block_size;
-        mbar_arrive_expect_tx(&bars[st], (second || !two) ? Smem::STAGE_BYTES : Smem::STAGE_BYTES / 2);
+        mbar_arrive_expect_tx(&bars[st], whole ? Smem::STAGE_BYTES : Smem::STAGE_BYTES / 2);
         tma_load_2d(kd, &tmap_k, 0, r0, &bars[st]);
         tma_load_2d(vd, &tmap_v, 0, r0, &bars[st]);
         if (second) {
@@ -441,8 +595,9 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
   };
   for (int k = 0; k < STAGES; ++k) issue_next();
 
-  Math8<E, D> cm;
-  int L = 0, hq0 = 0, slot = 0;
+  Math8<E, D, FEW> cm;
+  RowGroup g{};
+  int hq0 = 0, slot = 0;
   bool full = false, piece_bad = false;
   int cons_left = plan.length(cons_c);
   int k = 0;  // tile index within the consumer's chunk
@@ -459,10 +614,10 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
       full = (cp.j == 0 && len == cp.nt);
       slot = (k == 0) ? 0 : 1;
       hq0 = chunk_first_head(a, cp.hc);
-      const bool q_ok = dcheck(cp.s < S && hq0 + G <= a.num_q_heads);
-      L = q_ok ? __ldg(a.context_lens + cp.s) : 0;
+      const bool q_ok = dcheck(cp.s < S && hq0 + col.G <= a.num_q_heads);
+      if (q_ok) g = row_group<FEW>(args, cp.s);
       piece_bad = false;
-      cm.begin(a.q + (long long)cp.s * a.q_seq_stride + (long long)hq0 * D, G, q_ok, a.scale_log2, lane);
+      cm.begin(args, g, hq0, q_ok, col);
     }
     const int st = (int)(iter % STAGES);
     if (!wait_slot<STAGES>(bars, iter, (int)(issued - iter), a.wait_limit_ns, lane)) return;
@@ -470,7 +625,8 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     if (!piece_bad) {
       const uint32_t kt = smem_addr(ring + st * Smem::STAGE_BYTES);
       const float4 sc4 = *reinterpret_cast<const float4 *>(scales + st * 4);
-      cm.tile(kt, kt + Smem::TILE_BYTES, sc4, min(TILE8, L - cp.j * TILE8), lane);
+      const int j0 = cp.j * TILE8;
+      cm.tile(kt, kt + Smem::TILE_BYTES, sc4, min(TILE8, g.L - j0), j0, lane);
     }
     __syncwarp();
     issue_next();
@@ -478,40 +634,320 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
 
     if (cp.j + 1 == cp.nt || cons_left == 1) {  // end of the piece
       if (piece_bad && lane == 0) atomicOr(&g_status, PA_DEV_ERR_BLOCK_ID);
-      const int gid = lane >> 2, ha = 2 * (lane & 3), hb = ha + 1;
       if (full) {
-        const float ia = 1.f / cm.la, ib = 1.f / cm.lb;
-        uint16_t *orow = a.out + (long long)cp.s * a.out_seq_stride + (long long)hq0 * D + 2 * gid;
-        if (dcheck(cp.s < S && hq0 + G <= a.num_q_heads)) {
-#pragma unroll
-          for (int c = 0; c < KSTEPS; ++c) {
-            if (ha < G)
-              *reinterpret_cast<uint32_t *>(orow + ha * D + 16 * c) =
-                  piece_bad ? 0u : E::narrow2(cm.o[c][0] * ia, cm.o[c][2] * ia);
-            if (hb < G)
-              *reinterpret_cast<uint32_t *>(orow + hb * D + 16 * c) =
-                  piece_bad ? 0u : E::narrow2(cm.o[c][1] * ib, cm.o[c][3] * ib);
-          }
-        }
+        if (dcheck(cp.s < S && hq0 + col.G <= a.num_q_heads)) cm.store_output(args, g, hq0, piece_bad, col);
       } else if (dcheck(cons_c < a.max_chunks)) {
-        const long long prow = (cons_c * 2 + slot) * G;
+        const long long prow = (cons_c * 2 + slot) * C;
+        const int ca = 2 * col.tig, cb = ca + 1;
         if (!piece_bad) {
-          float *acc = a.ws_acc + prow * D + 2 * gid;
+          float *acc = a.ws_acc + prow * D + 2 * col.gid;
 #pragma unroll
           for (int c = 0; c < KSTEPS; ++c) {
-            if (ha < G) *reinterpret_cast<float2 *>(acc + ha * D + 16 * c) = make_float2(cm.o[c][0], cm.o[c][2]);
-            if (hb < G) *reinterpret_cast<float2 *>(acc + hb * D + 16 * c) = make_float2(cm.o[c][1], cm.o[c][3]);
+            if (ca < C) *reinterpret_cast<float2 *>(acc + ca * D + 16 * c) = make_float2(cm.o[c][0], cm.o[c][2]);
+            if (cb < C) *reinterpret_cast<float2 *>(acc + cb * D + 16 * c) = make_float2(cm.o[c][1], cm.o[c][3]);
           }
         }
-        if (gid == 0) {
-          if (ha < G) a.ws_ml[prow + ha] = piece_bad ? make_float2(-INFINITY, -1.f) : make_float2(cm.ma, cm.la);
-          if (hb < G) a.ws_ml[prow + hb] = piece_bad ? make_float2(-INFINITY, -1.f) : make_float2(cm.mb, cm.lb);
+        if (col.gid == 0) {
+          if (ca < C) a.ws_ml[prow + ca] = piece_bad ? make_float2(-INFINITY, -1.f) : make_float2(cm.ma, cm.la);
+          if (cb < C) a.ws_ml[prow + cb] = piece_bad ? make_float2(-INFINITY, -1.f) : make_float2(cm.mb, cm.lb);
         }
       }
     }
     advance_tile(cp, pt, S, HC);
     --cons_left;
     ++k;
+  }
+}
+
+// One warp per HW columns of a unit: the zero rows of groups without a context (with the status bits of invalid
+// inputs), and the merge of the pieces of units that the split kernel cut:
+//   out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p,  M = max_p m_p,
+// in increasing chunk order (deterministic).  As decode_merge_kernel, for units whose columns are several tokens.
+template <class E, int D, int HW, int MB, bool FEW>
+__global__ void __launch_bounds__(256, 1) decode8_merge_kernel(const Decode8Args args) {
+  static_assert(32 % MB == 0, "a batch of pieces never straddles a 32-piece window");
+  const DecodeArgs &a = args.d;
+  constexpr int DPL = D / 32;  // dims per lane (4 or 2)
+  const int lane = threadIdx.x & 31;
+  grid_dependency_wait();  // the split kernel's pieces and tile prefix
+  grid_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ws_queue = 0ull;  // leave the chunk counter clear
+  const int S = a.num_seqs, HC = a.num_kv_heads * a.n_chunks, G = a.heads_per_unit, C = FEW ? args.tokens * G : G;
+  const int subs = C / HW;  // warps per unit
+  const long long w = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+  if (w >= (long long)S * HC * subs) return;
+  const long long seg = w / subs;
+  const int c0 = (int)(w - seg * subs) * HW;  // first column of this warp
+  const int v = (int)(seg / HC), hc = (int)(seg - (long long)v * HC);
+  const int pt0 = __ldg(a.ws_tiles + v), pt1 = __ldg(a.ws_tiles + v + 1), pts = __ldg(a.ws_tiles + S);
+  const RowGroup g = row_group<FEW>(args, v);
+  if (lane == 0 && hc == 0 && c0 == 0) {
+    const unsigned err = row_group_errors<FEW>(args, v);
+    if (err) atomicOr(&g_status, err);
+  }
+  if (c0 / G >= g.cnt) return;  // columns of no token
+  float o[HW][DPL];
+#pragma unroll
+  for (int x = 0; x < HW; ++x)
+#pragma unroll
+    for (int k = 0; k < DPL; ++k) o[x][k] = 0.f;
+  if (g.L > 0) {
+    const ChunkPlan plan = plan_chunks8(a, pts);
+    const int nt = pt1 - pt0;
+    const long long seg0 = (long long)pt0 * HC + (long long)hc * nt;
+    if (!dcheck(nt > 0 && pt0 >= 0 && pt1 <= pts)) return;  // a group with a context owns tiles
+    const long long c_first = plan.chunk_of(seg0), c_last = plan.chunk_of(seg0 + nt - 1);
+    if (c_first == c_last) return;  // one chunk held the whole unit: the split kernel wrote the rows
+    if (!dcheck(c_first >= 0 && c_last < plan.count && c_last < a.max_chunks)) return;
+    const int n = (int)(c_last - c_first + 1);
+    const int first_slot = seg0 > plan.start(c_first) ? 1 : 0;
+    auto piece_row = [&](int p) -> long long {  // partial row of this warp's first column in piece p
+      return ((c_first + p) * 2 + (p == 0 ? first_slot : 0)) * C + c0;
+    };
+    // (m, l) of the first 32 pieces (lane p holds piece p) and the partial rows of the first batch, together
+    float2 ml0[HW];
+#pragma unroll
+    for (int x = 0; x < HW; ++x) ml0[x] = make_float2(-INFINITY, 0.f);
+    if (lane < n) {
+      const long long r = piece_row(lane);
+#pragma unroll
+      for (int x = 0; x < HW; ++x) ml0[x] = __ldg(a.ws_ml + r + x);
+    }
+    float t[MB][HW][DPL];
+    auto load_batch = [&](int base) {
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const bool ok = base + i < n;
+        const long long r = ok ? piece_row(base + i) : 0;
+#pragma unroll
+        for (int x = 0; x < HW; ++x) {
+          const float *src = a.ws_acc + (r + x) * D + lane * DPL;
+          if constexpr (DPL == 4) {
+            const float4 q = ok ? __ldg(reinterpret_cast<const float4 *>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            t[i][x][0] = q.x;
+            t[i][x][1] = q.y;
+            t[i][x][2] = q.z;
+            t[i][x][3] = q.w;
+          } else {
+            const float2 q = ok ? __ldg(reinterpret_cast<const float2 *>(src)) : make_float2(0.f, 0.f);
+            t[i][x][0] = q.x;
+            t[i][x][1] = q.y;
+          }
+        }
+      }
+    };
+    load_batch(0);
+    // maximum and validity over all pieces, per column
+    float M[HW];
+    bool err = false;
+#pragma unroll
+    for (int x = 0; x < HW; ++x) {
+      M[x] = ml0[x].x;
+      err |= lane < n && ml0[x].y < 0.f;
+    }
+    for (int p = lane + 32; p < n; p += 32) {
+      const long long r = piece_row(p);
+#pragma unroll
+      for (int x = 0; x < HW; ++x) {
+        const float2 ml = __ldg(a.ws_ml + r + x);
+        M[x] = fmaxf(M[x], ml.x);
+        err |= ml.y < 0.f;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < HW; ++x)
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) M[x] = fmaxf(M[x], __shfl_xor_sync(FULL, M[x], off));
+    if (!__any_sync(FULL, err)) {
+      // lane p of the current 32-piece window holds piece p's weight per column; weighted l sums run per lane
+      float wt[HW], l[HW];
+#pragma unroll
+      for (int x = 0; x < HW; ++x) {
+        wt[x] = lane < n ? exp2f(ml0[x].x - M[x]) : 0.f;
+        l[x] = ml0[x].y * wt[x];
+      }
+      for (int base = 0; base < n; base += MB) {
+        if (base > 0) {
+          if ((base & 31) == 0) {  // next window of 32 pieces: their (m, l)
+            const int p = base + lane;
+            const long long r = p < n ? piece_row(p) : 0;
+#pragma unroll
+            for (int x = 0; x < HW; ++x) {
+              const float2 ml = p < n ? __ldg(a.ws_ml + r + x) : make_float2(-INFINITY, 0.f);
+              wt[x] = p < n ? exp2f(ml.x - M[x]) : 0.f;
+              l[x] = fmaf(ml.y, wt[x], l[x]);
+            }
+          }
+          load_batch(base);
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          const int src_lane = (base + i) & 31;
+#pragma unroll
+          for (int x = 0; x < HW; ++x) {
+            const float wq = __shfl_sync(FULL, wt[x], src_lane);  // 0 past the last piece
+#pragma unroll
+            for (int k = 0; k < DPL; ++k) o[x][k] = fmaf(wq, t[i][x][k], o[x][k]);
+          }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < HW; ++x) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) l[x] += __shfl_xor_sync(FULL, l[x], off);
+#pragma unroll
+        for (int k = 0; k < DPL; ++k) o[x][k] = o[x][k] / l[x];
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < HW; ++x) {
+    const int tok = (c0 + x) / G, head = chunk_first_head(a, hc) + (c0 + x) - tok * G;
+    if (tok >= g.cnt) break;
+    uint16_t *dst = a.out + (long long)(g.tok + tok) * a.out_seq_stride + (long long)head * D + lane * DPL;
+    if constexpr (DPL == 4) {
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(E::narrow2(o[x][0], o[x][1]), E::narrow2(o[x][2], o[x][3]));
+    } else {
+      *reinterpret_cast<uint32_t *>(dst) = E::narrow2(o[x][0], o[x][1]);
+    }
+  }
+}
+
+// Small calls: one block per unit, its WARPS warps take the unit's tiles in turn (tile j to warp j mod WARPS), and
+// their softmax states are merged in shared memory, in warp order (deterministic).  No workspace, no tensor map, no
+// second launch: chosen when all units fit one wave of blocks and none is long, where the split kernel's tile prefix,
+// queue and merge would cost more than the work.  Tiles come in by 16-byte asynchronous copies, placed as TMA's
+// swizzle would.
+template <int D, int WARPS>
+struct SegSmem8 {
+  static constexpr int STAGES = 2;
+  static constexpr uint32_t TILE_BYTES = TILE8 * D;
+  static constexpr uint32_t STAGE_BYTES = 2 * TILE_BYTES + 16;  // and the tile's four scales
+  static constexpr uint32_t RING = WARPS * STAGES * STAGE_BYTES;
+  static constexpr uint32_t MERGE = WARPS * 8 * (D + 2) * 4 + WARPS * 4;
+  static constexpr uint32_t BYTES = RING > MERGE ? RING : MERGE;
+};
+
+template <class E, int D, int WARPS, bool FEW>
+__global__ void __launch_bounds__(WARPS * 32) decode8_segment_kernel(const Decode8Args args) {
+  const DecodeArgs &a = args.d;
+  using Smem = SegSmem8<D, WARPS>;
+  constexpr int KSTEPS = D / 16, CPR = D / 16;  // 16-byte pieces of a row
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dependency_wait();  // every input may come from the previous kernel in the stream
+  grid_launch_dependents();
+  const int HC = a.num_kv_heads * a.n_chunks;
+  const int v = (int)(blockIdx.x / HC), hc = (int)(blockIdx.x - (unsigned)v * HC);
+  const int hq0 = chunk_first_head(a, hc), h = hc / a.n_chunks;
+  const Columns<FEW> col(a.heads_per_unit, lane);
+  const RowGroup g = row_group<FEW>(args, v);
+  if (hc == 0 && threadIdx.x == 0) {
+    const unsigned err = row_group_errors<FEW>(args, v);
+    if (err) atomicOr(&g_status, err);
+  }
+  const int C = g.cnt * col.G;  // live columns
+  const int nt = group_tiles(g);
+  auto out_row = [&](int c) {
+    const int tok = c / col.G;
+    return a.out + (long long)(g.tok + tok) * a.out_seq_stride + (long long)(hq0 + c - tok * col.G) * D;
+  };
+  if (nt == 0) {  // zero rows, or none
+    for (int i = threadIdx.x; i < C * (D / 8); i += WARPS * 32)
+      reinterpret_cast<uint4 *>(out_row(i / (D / 8)))[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const int mine = warp < nt ? (nt - warp + WARPS - 1) / WARPS : 0;
+  unsigned char *ring = smem + warp * Smem::STAGES * Smem::STAGE_BYTES;
+  TileLookup look;
+  bool bad = false;
+  // this warp's t-th tile into slot t % 2; rows of a missing half are left alone (the arithmetic clears them)
+  auto fetch = [&](int t) {
+    const int j = warp + t * WARPS;
+    int p0, p1;
+    bool second;
+    const bool good = look.find(a, g.s, nt, j, g.L, lane, &p0, &p1, &second) && dcheck(h < a.num_kv_heads);
+    bad |= !good;
+    unsigned char *kd = ring + (t % Smem::STAGES) * Smem::STAGE_BYTES;
+    if (good) {
+      const int rows = second || a.block_size != 16 ? TILE8 : 16;
+      const long long s0 = (long long)p0 * a.num_kv_heads + h, s1 = (long long)p1 * a.num_kv_heads + h;
+      // row 16 + r of the tile: row r of the second block, or of the block's second half
+      const long long b0 = s0 * a.block_size * D, b1 = a.block_size == 16 ? s1 * 16 * D : b0 + 16 * D;
+#pragma unroll
+      for (int i = 0; i < TILE8 * CPR / 32; ++i) {
+        const int r = (i * 32 + lane) / CPR, c = (i * 32 + lane) % CPR;
+        if (r >= rows) break;
+        const long long src = (r < 16 ? b0 + r * D : b1 + (r - 16) * D) + c * 16;
+        const uint32_t at = swizzled8<D>(r, c);
+        cp_async16(kd + at, args.k_cache + src, true);
+        cp_async16(kd + Smem::TILE_BYTES + at, args.v_cache + src, true);
+      }
+      if (lane < 4) {
+        if (!(lane & 1) || rows == TILE8)
+          cp_async4(kd + 2 * Smem::TILE_BYTES + lane * 4,
+                    ((lane & 2) ? args.v_scale : args.k_scale) + ((lane & 1) ? s1 : s0));
+      }
+    }
+    cp_async_commit();
+  };
+  if (mine > 0) fetch(0);
+  Math8<E, D, FEW> cm;
+  cm.begin(args, g, hq0, dcheck(hq0 + col.G <= a.num_q_heads), col);
+  for (int t = 0; t < mine && !bad; ++t) {
+    if (t + 1 < mine) {
+      fetch(t + 1);
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
+    }
+    __syncwarp();
+    const unsigned char *kd = ring + (t % Smem::STAGES) * Smem::STAGE_BYTES;
+    const float4 sc4 = *reinterpret_cast<const float4 *>(kd + 2 * Smem::TILE_BYTES);
+    const int j0 = (warp + t * WARPS) * TILE8;
+    cm.tile(smem_addr(kd), smem_addr(kd) + Smem::TILE_BYTES, sc4, min(TILE8, g.L - j0), j0, lane);
+    __syncwarp();
+  }
+  cp_async_wait<0>();
+  // the warps' states through shared memory (every copy has landed)
+  __syncthreads();
+  float *x_acc = reinterpret_cast<float *>(smem);  // [WARPS][8][D]
+  float2 *x_ml = reinterpret_cast<float2 *>(x_acc + WARPS * 8 * D);
+  int *x_bad = reinterpret_cast<int *>(x_ml + WARPS * 8);
+  float *acc = x_acc + (warp * 8 + 2 * col.tig) * D + 2 * col.gid;
+#pragma unroll
+  for (int c = 0; c < KSTEPS; ++c) {
+    *reinterpret_cast<float2 *>(acc + 16 * c) = make_float2(cm.o[c][0], cm.o[c][2]);
+    *reinterpret_cast<float2 *>(acc + D + 16 * c) = make_float2(cm.o[c][1], cm.o[c][3]);
+  }
+  if (col.gid == 0) {
+    x_ml[warp * 8 + 2 * col.tig] = make_float2(cm.ma, cm.la);
+    x_ml[warp * 8 + 2 * col.tig + 1] = make_float2(cm.mb, cm.lb);
+  }
+  if (lane == 0) x_bad[warp] = bad ? 1 : 0;
+  __syncthreads();
+  bool any_bad = false;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) any_bad |= x_bad[w] != 0;
+  if (any_bad && threadIdx.x == 0) atomicOr(&g_status, PA_DEV_ERR_BLOCK_ID);
+  for (int i = threadIdx.x; i < C * (D / 8); i += WARPS * 32) {
+    const int c = i / (D / 8), d0 = (i % (D / 8)) * 8;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, x_ml[w * 8 + c].x);
+    float l = 0.f, f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float2 ml = x_ml[w * 8 + c];
+      const float wt = ml.y != 0.f ? exp2f(ml.x - M) : 0.f;  // a warp without keys for this column: m = -inf, l = 0
+      l = fmaf(ml.y, wt, l);
+      const float *src = x_acc + (w * 8 + c) * D + d0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = fmaf(wt, src[e], f[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = any_bad ? 0.f : f[e] / l;
+    *reinterpret_cast<uint4 *>(out_row(c) + d0) = narrow8<E>(f);
   }
 }
 

@@ -225,7 +225,8 @@ def test_refusals_and_empty_batch():
         lambda: pa.decode_fp8(q, kc, vc, ks, vs, t, c, 0.1, 30, partition_tokens=8),
         lambda: pa.decode_fp8(q, kc, vc, ks, vs, t, c, 0.1, -1),
         lambda: pa.decode_fp8(q, kc, vc, ks, vs, t, c, 0.1, 30, out=q[:, :2]),
-        lambda: pa.decode_fp8(q, kc, vc, ks, vs, t, c, 0.1, 30, workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
+        lambda: pa.decode_fp8(q, kc, vc, ks, vs, t, c, 0.1, 30, partition_tokens=32,
+                              workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
     ]
     for call in bad:
         with pytest.raises(E):
