@@ -829,7 +829,7 @@ struct SegSmem8 {
 };
 
 template <class E, int D, int WARPS, bool FEW>
-__global__ void __launch_bounds__(WARPS * 32) decode8_segment_kernel(const Decode8Args args) {
+__global__ void __launch_bounds__(WARPS * 32, 3) decode8_segment_kernel(const Decode8Args args) {
   const DecodeArgs &a = args.d;
   using Smem = SegSmem8<D, WARPS>;
   constexpr int KSTEPS = D / 16, CPR = D / 16;  // 16-byte pieces of a row

@@ -2,7 +2,7 @@
 //
 // The pipeline of prefill_tc_kernel (two 128-row sub-tiles of one query head
 // against 128-key tiles, tcgen05 with accumulators in tensor memory, one
-// softmax warpgroup per sub-tile), with the page tiles brought in by three
+// softmax warpgroup per sub-tile), with the page tiles brought in by seven
 // loader warps instead of TMA: they read e4m3 rows (16 bytes a lane, whole
 // 128-byte lines a warp), widen them, multiply by the block's scale in fp32,
 // round to the storage type and store them in the 128-byte swizzle the tensor
@@ -13,9 +13,7 @@
 // stored as zeros whatever the pool holds there.
 //
 // Why not the tensor cores' own 8-bit kinds: they would need Q and P in 8 bits
-// too.  A 128-key tile of K and V is 32,768 values, about 90 instructions per
-// value pair and lane over the three warps, in the about 4,300 cycles that the
-// two sub-tiles' products and softmax take: the loaders stay ahead.
+// too.
 //
 // Work items are taken from a counter in the call's workspace.  The warp that
 // takes an item checks all of its table entries first, so that the other roles
@@ -34,10 +32,22 @@ struct Prefill8Args {
   float k_sign;  // sign of the softmax scale (0 for a scale of 0), multiplied into K: p.scale_log2 is then positive
 };
 
-constexpr int PF8_THREADS = 12 * 32;  // 8 softmax warps, 8 / 9 / 11 loaders, 10 MMA issue
-constexpr int PF8_LOADERS = 3;
-constexpr int PF8_ITEM_READERS = 11;  // two loaders, MMA lane, 8 softmax warps
+constexpr int PF8_THREADS = 16 * 32;  // 8 softmax warps, 8 / 9 / 11-15 loaders, 10 MMA issue
+constexpr int PF8_LOADERS = 7;
+constexpr int PF8_ITEM_READERS = 15;  // six loaders, MMA lane, 8 softmax warps
+// Registers per thread: 128 at launch (512 threads fill the file); the two softmax warpgroups take 40 more each from
+// the two others: 256 * 168 + 256 * 88 = 512 * 128.
+constexpr int PF8_SOFTMAX_REGS = 168, PF8_OTHER_REGS = 88;
 constexpr int PF8_QUARTERS = 4;       // a K or V tile is brought in as four units of 32 rows
+
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // Two fp32 values to the storage type, saturating (a re-scaled byte can pass fp16's largest value by a rounding).
 template <class E>
@@ -50,14 +60,46 @@ __device__ __forceinline__ uint32_t narrow2_sat(float lo, float hi) {
   return E::narrow2(lo, hi);
 }
 
-// One unit: 32 rows of a K or V tile, held by the warp as 16-byte pieces.
+// Two e4m3 values times a scale, in the storage type.  `s16`: the scale in fp16 when FAST (it is then exact there and
+// no product overflows): fp16 by one packed product, bf16 by mixed-precision ones.
+template <class E, bool FAST>
+__device__ __forceinline__ uint32_t scaled2(uint16_t x, float s, uint32_t s16) {
+  const uint32_t h = e4m3x2_to_f16x2(x);
+  if constexpr (FAST && std::is_same<E, F16>::value) {
+    const __half2 p = __hmul2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&s16));
+    return *reinterpret_cast<const uint32_t *>(&p);
+  } else if constexpr (FAST) {
+    float lo, hi;
+    asm("{\n\t.reg .b16 a, b, s, t;\n\tmov.b32 {a, b}, %2;\n\tmov.b32 {s, t}, %3;\n\t"
+        "fma.rn.f32.f16 %0, a, s, 0f00000000;\n\tfma.rn.f32.f16 %1, b, s, 0f00000000;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h), "r"(s16));
+    return E::narrow2(lo, hi);
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return narrow2_sat<E>(f.x * s, f.y * s);
+  }
+}
+// Whether a scale is an exact fp16 power of two (or zero) whose products with e4m3 values stay below fp16's largest
+// value and normal scale: |s| in [2^-14, 2^7].
+__device__ __forceinline__ bool scale_is_plain(float s) {
+  const float a = fabsf(s);
+  return s == 0.f || ((__float_as_uint(s) & 0x7fffffu) == 0 && a >= 6.103515625e-5f && a <= 128.f);
+}
+
+// One unit: 32 rows of a K or V tile, held by the warp as pieces of 16 bytes, each as two of 8 in the order in which
+// they are stored.
 template <class E, int D>
 struct LoadUnit {
   static constexpr int LPR = D / 16;       // lanes of a row
   static constexpr int N = LPR;            // pieces per lane: 32 rows * LPR / 32 lanes
   static constexpr int STEP = 32 / LPR;    // rows between a lane's pieces
-  uint4 w[N];
+  uint2 w[N][2];
   float s[2];  // scales of rows 0-15 and 16-31
+
+  // A piece's halves go to chunks 2 cc and 2 cc + 1 of its 64-element region; lanes of the second region store the
+  // odd one first, so that the eight lanes of a row meet all banks once.
+  static __device__ __forceinline__ int first_half(int lane) { return (lane % LPR) >> 2; }
 
   // Rows tok0 .. tok0 + 31 of the item's context; p0, p1: physical blocks of the two halves (-1: past the context).
   __device__ __forceinline__ void load(const uint8_t *cache, const float *scale, const PrefillArgs &a, int h, int p0,
@@ -66,42 +108,46 @@ struct LoadUnit {
     const long long slab0 = (long long)p0 * a.num_kv_heads + h, slab1 = (long long)p1 * a.num_kv_heads + h;
     s[0] = p0 >= 0 ? __ldg(scale + slab0) : 0.f;
     s[1] = p1 >= 0 ? __ldg(scale + slab1) : 0.f;
-    const int off = (lane / LPR) * D + (lane % LPR) * 16;
+    const int off = (lane / LPR) * D + (lane % LPR) * 16 + first_half(lane) * 8, other = 8 - 16 * first_half(lane);
     const uint8_t *half0 = cache + slab0 * a.block_size * D + off;
     const uint8_t *half1 = cache + slab1 * a.block_size * D + (a.block_size == 16 ? 0 : 16 * D) + off;
     const int live = kmax - tok0 - lane / LPR;  // rows of this lane's column that lie in the context
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      w[i] = i * STEP < live ? __ldg(reinterpret_cast<const uint4 *>((i < N / 2 ? half0 : half1) + (i % (N / 2)) * STEP * D))
-                             : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < N; ++i) {
+      const uint8_t *src = (i < N / 2 ? half0 : half1) + (i % (N / 2)) * STEP * D;
+      w[i][0] = w[i][1] = make_uint2(0, 0);
+      if (i * STEP < live) {
+        w[i][0] = __ldg(reinterpret_cast<const uint2 *>(src));
+        w[i][1] = __ldg(reinterpret_cast<const uint2 *>(src + other));
+      }
+    }
+  }
+  template <bool FAST>
+  __device__ __forceinline__ void store_as(uint8_t *tile, int row0, float s0, float s1, int lane) const {
+    uint8_t *region = tile + ((lane % LPR) / 4) * 128 * 128;
+    const int c0 = ((lane % LPR) % 4) * 2, f = first_half(lane);
+    const uint32_t h0 = F16::narrow2(s0, s0), h1 = F16::narrow2(s1, s1);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float sc = i < N / 2 ? s0 : s1;
+      const uint32_t hc = i < N / 2 ? h0 : h1;
+      const int row = row0 + i * STEP + lane / LPR, sw = row & 7;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint2 x = w[i][k];
+        *reinterpret_cast<uint4 *>(region + row * 128 + (((c0 + (k ^ f)) ^ sw) << 4)) =
+            make_uint4(scaled2<E, FAST>((uint16_t)x.x, sc, hc), scaled2<E, FAST>((uint16_t)(x.x >> 16), sc, hc),
+                       scaled2<E, FAST>((uint16_t)x.y, sc, hc), scaled2<E, FAST>((uint16_t)(x.y >> 16), sc, hc));
+      }
+    }
   }
   // Into rows row0 .. row0 + 31 of a tile stored as D / 64 regions of [128 rows][128 bytes], swizzled.
   __device__ __forceinline__ void store(uint8_t *tile, int row0, float factor, int lane) const {
-    const int cc = lane % LPR;  // dims 16 cc .. 16 cc + 15: chunks 2 cc and 2 cc + 1 of their 64-element region
-    uint8_t *region = tile + (cc / 4) * 128 * 128;
-    const int c0 = (cc % 4) * 2;
-    const float2 s0 = make_float2(s[0] * factor, s[0] * factor), s1 = make_float2(s[1] * factor, s[1] * factor);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float2 sc = i < N / 2 ? s0 : s1;
-      const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-      uint32_t o[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 a = __fmul2_rn(e4m3x2_to_float2((uint16_t)in[j]), sc);
-        const float2 b = __fmul2_rn(e4m3x2_to_float2((uint16_t)(in[j] >> 16)), sc);
-        o[2 * j] = narrow2_sat<E>(a.x, a.y);
-        o[2 * j + 1] = narrow2_sat<E>(b.x, b.y);
-      }
-      const int row = row0 + i * STEP + lane / LPR;
-      uint8_t *dst = region + row * 128;
-      const int sw = row & 7;
-      // lanes of the second region store their odd chunk first: the eight lanes of a row then meet all banks once
-      const bool odd = cc >= 4;
-      const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-      *reinterpret_cast<uint4 *>(dst + (((c0 + (odd ? 1 : 0)) ^ sw) << 4)) = odd ? hi : lo;
-      *reinterpret_cast<uint4 *>(dst + (((c0 + (odd ? 0 : 1)) ^ sw) << 4)) = odd ? lo : hi;
-    }
+    const float s0 = s[0] * factor, s1 = s[1] * factor;
+    if (scale_is_plain(s0) && scale_is_plain(s1))  // uniform
+      store_as<true>(tile, row0, s0, s1, lane);
+    else
+      store_as<false>(tile, row0, s0, s1, lane);
   }
 };
 
@@ -182,9 +228,10 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
     return ok;
   };
 
-  if (warp == 8 || warp == 9 || warp == 11) {
+  if (warp >= 8 && warp != 10) {
     // ------------------------------------------------------------ loaders (warp 8 also takes the items and loads Q)
-    const int w = warp == 11 ? 2 : warp - 8;
+    give_registers<PF8_OTHER_REGS>();
+    const int w = warp > 10 ? warp - 9 : warp - 8;
     if (w == 0 && lane == 0) prefetch_tensor_map(&tmap_q);
     long long g = 0;  // K/V tiles of the items before
     int n_items = 0;
@@ -276,10 +323,9 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
       };
       const int units = it.nt * 8;
       const int u0 = (int)((w + PF8_LOADERS - (g * 8) % PF8_LOADERS) % PF8_LOADERS);
-      LoadUnit<E, D> cur, next;
-      if (u0 < units) load(u0, cur);
+      LoadUnit<E, D> x;
       for (int u = u0; u < units; u += PF8_LOADERS) {
-        if (u + PF8_LOADERS < units) load(u + PF8_LOADERS, next);  // in flight while this unit is converted
+        load(u, x);  // in flight while the slot is waited for
         const long long t = g + (u >> 3);
         const bool is_v = (u >> 2) & 1;
         const int nst = is_v ? PF_VST : PF_KST;
@@ -289,11 +335,10 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
           ok = false;
           break;
         }
-        cur.store(sm + (is_v ? L::V : L::K) + st * HALVES * REGION, (u & 3) * 32, is_v ? 1.f : args.k_sign, lane);
+        x.store(sm + (is_v ? L::V : L::K) + st * HALVES * REGION, (u & 3) * 32, is_v ? 1.f : args.k_sign, lane);
         fence_proxy_async_smem();  // the tensor cores read the rows through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive(&(is_v ? v_full : k_full)[st]);
-        cur = next;
       }
       g += it.nt;
       ++n_items;
@@ -307,6 +352,7 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
       atomicOr(&g_status, PA_DEV_ERR_TIMEOUT);
   } else if (warp == 10) {
     // ------------------------------------------------------------ MMA issue (one lane)
+    give_registers<PF8_OTHER_REGS>();
     if (lane == 0) {
       constexpr uint32_t idesc_qk = tc::idesc_f16(kBf16, false, PF_BM, PF_BN);
       constexpr uint32_t idesc_pv = tc::idesc_f16(kBf16, true, PF_BM, D);
@@ -395,6 +441,7 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax and epilogue of sub-tile x (warps 0-3: A, 4-7: B)
+    take_registers<PF8_SOFTMAX_REGS>();
     const int x = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
