@@ -1651,11 +1651,11 @@ int pa_prefill_fp8(const void *q, const void *k_cache, const void *v_cache, cons
     return finish_launch(launch_pdl(kernel, grid, dim3(pa::PF8_THREADS), smem, st, mq, args));
   };
   if (dtype == PA_BFLOAT16) {
-    if (head_dim == 128) return launch(pa::prefill8_tc_kernel<pa::BF16, 128>, pa::PrefillSmem<128>::ALLOC);
-    return launch(pa::prefill8_tc_kernel<pa::BF16, 64>, pa::PrefillSmem<64>::ALLOC);
+    if (head_dim == 128) return launch(pa::prefill8_tc_kernel<pa::BF16, 128>, pa::Prefill8Smem<128>::ALLOC);
+    return launch(pa::prefill8_tc_kernel<pa::BF16, 64>, pa::Prefill8Smem<64>::ALLOC);
   }
-  if (head_dim == 128) return launch(pa::prefill8_tc_kernel<pa::F16, 128>, pa::PrefillSmem<128>::ALLOC);
-  return launch(pa::prefill8_tc_kernel<pa::F16, 64>, pa::PrefillSmem<64>::ALLOC);
+  if (head_dim == 128) return launch(pa::prefill8_tc_kernel<pa::F16, 128>, pa::Prefill8Smem<128>::ALLOC);
+  return launch(pa::prefill8_tc_kernel<pa::F16, 64>, pa::Prefill8Smem<64>::ALLOC);
 }
 
 int pa_read_bandwidth_probe(const void *src, int64_t bytes, uint32_t *sink, void *stream) {

@@ -35,10 +35,31 @@ struct Prefill8Args {
 constexpr int PF8_THREADS = 16 * 32;  // 8 softmax warps, 8 / 9 / 11-15 loaders, 10 MMA issue
 constexpr int PF8_LOADERS = 7;
 constexpr int PF8_ITEM_READERS = 15;  // six loaders, MMA lane, 8 softmax warps
-// Registers per thread: 128 at launch (512 threads fill the file); the two softmax warpgroups take 40 more each from
-// the two others: 256 * 168 + 256 * 88 = 512 * 128.
-constexpr int PF8_SOFTMAX_REGS = 168, PF8_OTHER_REGS = 88;
+// Registers per thread: 128 at launch (512 threads fill the file); the two softmax warpgroups take 48 more each from
+// the two others: 256 * 176 + 256 * 80 = 512 * 128.
+constexpr int PF8_SOFTMAX_REGS = 176, PF8_OTHER_REGS = 80;
 constexpr int PF8_QUARTERS = 4;       // a K or V tile is brought in as four units of 32 rows
+
+// Rings of K and V tiles.  What shared memory does not take is L1, which the loaders' 16-byte reads want: a third slot
+// for K or for V cost more than it gave (792 and 785 against 735 us for 32 chunks of 512 tokens).
+constexpr int PF8_KST = 2, PF8_VST = 2;
+
+template <int D>
+struct Prefill8Smem {
+  static constexpr uint32_t REGION = 128 * 128;  // 128 rows of 128 bytes (64 elements)
+  static constexpr uint32_t HALVES = D / 64;
+  static constexpr uint32_t Q = 0;  // sub-tiles A and B
+  static constexpr uint32_t K = Q + 2 * HALVES * REGION;
+  static constexpr uint32_t V = K + PF8_KST * HALVES * REGION;
+  static constexpr uint32_t BARS = V + PF8_VST * HALVES * REGION;
+  static constexpr uint32_t BYTES = BARS + 512;  // up to 29 mbarriers, the item ring, the tensor-memory address, flags
+  // + alignment slack; at least 120 KB so that one CTA holds an SM (and its tensor memory) alone
+  static constexpr uint32_t ALLOC = (BYTES + 1024 > 120 * 1024) ? BYTES + 1024 : 120 * 1024;
+  // tensor memory columns
+  static constexpr uint32_t T_S = 0;      // S_x at T_S + x * 128; P_x in its first 64 columns
+  static constexpr uint32_t T_O = 256;    // O_x at T_O + x * D
+};
+static_assert(Prefill8Smem<128>::ALLOC <= 232448, "prefill smem over the per-block opt-in limit");
 
 template <int N>
 __device__ __forceinline__ void take_registers() {
@@ -87,19 +108,14 @@ __device__ __forceinline__ bool scale_is_plain(float s) {
   return s == 0.f || ((__float_as_uint(s) & 0x7fffffu) == 0 && a >= 6.103515625e-5f && a <= 128.f);
 }
 
-// One unit: 32 rows of a K or V tile, held by the warp as pieces of 16 bytes, each as two of 8 in the order in which
-// they are stored.
+// One unit: 32 rows of a K or V tile, held by the warp as pieces of 16 bytes.
 template <class E, int D>
 struct LoadUnit {
   static constexpr int LPR = D / 16;       // lanes of a row
   static constexpr int N = LPR;            // pieces per lane: 32 rows * LPR / 32 lanes
   static constexpr int STEP = 32 / LPR;    // rows between a lane's pieces
-  uint2 w[N][2];
+  uint4 w[N];
   float s[2];  // scales of rows 0-15 and 16-31
-
-  // A piece's halves go to chunks 2 cc and 2 cc + 1 of its 64-element region; lanes of the second region store the
-  // odd one first, so that the eight lanes of a row meet all banks once.
-  static __device__ __forceinline__ int first_half(int lane) { return (lane % LPR) >> 2; }
 
   // Rows tok0 .. tok0 + 31 of the item's context; p0, p1: physical blocks of the two halves (-1: past the context).
   __device__ __forceinline__ void load(const uint8_t *cache, const float *scale, const PrefillArgs &a, int h, int p0,
@@ -108,24 +124,22 @@ struct LoadUnit {
     const long long slab0 = (long long)p0 * a.num_kv_heads + h, slab1 = (long long)p1 * a.num_kv_heads + h;
     s[0] = p0 >= 0 ? __ldg(scale + slab0) : 0.f;
     s[1] = p1 >= 0 ? __ldg(scale + slab1) : 0.f;
-    const int off = (lane / LPR) * D + (lane % LPR) * 16 + first_half(lane) * 8, other = 8 - 16 * first_half(lane);
+    const int off = (lane / LPR) * D + (lane % LPR) * 16;
     const uint8_t *half0 = cache + slab0 * a.block_size * D + off;
     const uint8_t *half1 = cache + slab1 * a.block_size * D + (a.block_size == 16 ? 0 : 16 * D) + off;
     const int live = kmax - tok0 - lane / LPR;  // rows of this lane's column that lie in the context
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint8_t *src = (i < N / 2 ? half0 : half1) + (i % (N / 2)) * STEP * D;
-      w[i][0] = w[i][1] = make_uint2(0, 0);
-      if (i * STEP < live) {
-        w[i][0] = __ldg(reinterpret_cast<const uint2 *>(src));
-        w[i][1] = __ldg(reinterpret_cast<const uint2 *>(src + other));
-      }
-    }
+    for (int i = 0; i < N; ++i)
+      w[i] = i * STEP < live ? __ldg(reinterpret_cast<const uint4 *>((i < N / 2 ? half0 : half1) + (i % (N / 2)) * STEP * D))
+                             : make_uint4(0, 0, 0, 0);
   }
+  // A piece becomes chunks c0 and c0 + 1 of its 64-element region.  The two regions' chunks of a row fall on the same
+  // banks (two-way conflicts); swapping the order for one region cost more in selects, or in 8-byte loads (734 and
+  // 749 against 729 us for 32 chunks of 512 tokens).
   template <bool FAST>
   __device__ __forceinline__ void store_as(uint8_t *tile, int row0, float s0, float s1, int lane) const {
     uint8_t *region = tile + ((lane % LPR) / 4) * 128 * 128;
-    const int c0 = ((lane % LPR) % 4) * 2, f = first_half(lane);
+    const int c0 = ((lane % LPR) % 4) * 2;
     const uint32_t h0 = F16::narrow2(s0, s0), h1 = F16::narrow2(s1, s1);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -134,8 +148,8 @@ struct LoadUnit {
       const int row = row0 + i * STEP + lane / LPR, sw = row & 7;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const uint2 x = w[i][k];
-        *reinterpret_cast<uint4 *>(region + row * 128 + (((c0 + (k ^ f)) ^ sw) << 4)) =
+        const uint2 x = k == 0 ? make_uint2(w[i].x, w[i].y) : make_uint2(w[i].z, w[i].w);
+        *reinterpret_cast<uint4 *>(region + row * 128 + (((c0 + k) ^ sw) << 4)) =
             make_uint4(scaled2<E, FAST>((uint16_t)x.x, sc, hc), scaled2<E, FAST>((uint16_t)(x.x >> 16), sc, hc),
                        scaled2<E, FAST>((uint16_t)x.y, sc, hc), scaled2<E, FAST>((uint16_t)(x.y >> 16), sc, hc));
       }
@@ -155,7 +169,7 @@ template <class E, int D>
 __global__ void __launch_bounds__(PF8_THREADS, 1)
     prefill8_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const Prefill8Args args) {
   const PrefillArgs &a = args.p;
-  using L = PrefillSmem<D>;
+  using L = Prefill8Smem<D>;
   constexpr int HALVES = D / 64;
   constexpr uint32_t REGION = L::REGION;
   constexpr bool kBf16 = std::is_same<E, BF16>::value;
@@ -169,11 +183,11 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BARS);
   uint64_t *q_full = bars;
   uint64_t *q_empty = q_full + 1;
-  uint64_t *k_full = q_empty + 1;       // [PF_KST]
-  uint64_t *k_empty = k_full + PF_KST;  // [PF_KST]
-  uint64_t *v_full = k_empty + PF_KST;  // [PF_VST]
-  uint64_t *v_empty = v_full + PF_VST;  // [PF_VST]
-  uint64_t *s_full = v_empty + PF_VST;  // [2]: S_A, S_B written (and every earlier MMA done)
+  uint64_t *k_full = q_empty + 1;       // [PF8_KST]
+  uint64_t *k_empty = k_full + PF8_KST;  // [PF8_KST]
+  uint64_t *v_full = k_empty + PF8_KST;  // [PF8_VST]
+  uint64_t *v_empty = v_full + PF8_VST;  // [PF8_VST]
+  uint64_t *s_full = v_empty + PF8_VST;  // [2]: S_A, S_B written (and every earlier MMA done)
   uint64_t *p_full = s_full + 2;        // [2]: P_A, P_B written
   uint64_t *o_done = p_full + 2;        // [2]: an item's last PV of A, of B done
   uint64_t *drained = o_done + 2;
@@ -187,11 +201,11 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int i = 0; i < PF_KST; ++i) {
+    for (int i = 0; i < PF8_KST; ++i) {
       mbar_init(&k_full[i], PF8_QUARTERS);
       mbar_init(&k_empty[i], 1);
     }
-    for (int i = 0; i < PF_VST; ++i) {
+    for (int i = 0; i < PF8_VST; ++i) {
       mbar_init(&v_full[i], PF8_QUARTERS);
       mbar_init(&v_empty[i], 1);
     }
@@ -328,7 +342,7 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
         load(u, x);  // in flight while the slot is waited for
         const long long t = g + (u >> 3);
         const bool is_v = (u >> 2) & 1;
-        const int nst = is_v ? PF_VST : PF_KST;
+        const int nst = is_v ? PF8_VST : PF8_KST;
         const int st = (int)(t % nst);
         if (t >= nst && !(ok = warp_wait(&(is_v ? v_empty : k_empty)[st], (uint32_t)(((t / nst) - 1) & 1), limit))) break;
         if (__any_sync(FULL, *abort_flag != 0)) {
@@ -363,7 +377,7 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
       bool ok = true;
       // S_x = Q_x K(t)^T
       auto issue_qk = [&](int x, long long t) {
-        const uint32_t ks = sbase + L::K + (uint32_t)(t % PF_KST) * HALVES * REGION;
+        const uint32_t ks = sbase + L::K + (uint32_t)(t % PF8_KST) * HALVES * REGION;
         const uint32_t qx = qs + x * HALVES * REGION;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -376,8 +390,8 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
       // O_x += P_x V(t), once softmax_x has written P_x for its tile gx
       auto issue_pv = [&](int x, long long t, long long tx, bool first_of_item) -> bool {
         if (!mbar_wait_bounded(&p_full[x], (uint32_t)(tx & 1), limit)) return false;
-        const int st = (int)(t % PF_VST);
-        if (!mbar_wait_bounded(&v_full[st], (uint32_t)((t / PF_VST) & 1), limit)) return false;
+        const int st = (int)(t % PF8_VST);
+        if (!mbar_wait_bounded(&v_full[st], (uint32_t)((t / PF8_VST) & 1), limit)) return false;
         tc::fence_after_sync();
         const uint32_t vs = sbase + L::V + st * HALVES * REGION;
 #pragma unroll
@@ -400,21 +414,21 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
             break;
           }
           const bool a_on = j < it.nt_a, b_on = it.has_b;
-          if (!(ok = mbar_wait_bounded(&k_full[g % PF_KST], (uint32_t)((g / PF_KST) & 1), limit))) break;
+          if (!(ok = mbar_wait_bounded(&k_full[g % PF8_KST], (uint32_t)((g / PF8_KST) & 1), limit))) break;
           tc::fence_after_sync();
           if (a_on) issue_qk(0, g);
           if (pend_t >= 0) {
             if (!(ok = issue_pv(1, pend_t, pend_tb, pend_first))) break;
-            tc::commit(&v_empty[pend_t % PF_VST]);
+            tc::commit(&v_empty[pend_t % PF8_VST]);
             pend_t = -1;
           }
           if (b_on) issue_qk(1, g);
-          tc::commit(&k_empty[g % PF_KST]);
+          tc::commit(&k_empty[g % PF8_KST]);
           if (j == it.nt - 1) tc::commit(q_empty);
           if (a_on) {
             if (!(ok = issue_pv(0, g, gx[0], j == 0))) break;
             if (j == it.nt_a - 1) tc::commit(&o_done[0]);
-            if (!b_on) tc::commit(&v_empty[g % PF_VST]);
+            if (!b_on) tc::commit(&v_empty[g % PF8_VST]);
             ++gx[0];
           }
           if (b_on) {
@@ -425,7 +439,7 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
         }
         if (ok && pend_t >= 0) {  // the item's last PV_B
           if ((ok = issue_pv(1, pend_t, pend_tb, pend_first))) {
-            tc::commit(&v_empty[pend_t % PF_VST]);
+            tc::commit(&v_empty[pend_t % PF8_VST]);
             tc::commit(&o_done[1]);
           }
         }
