@@ -531,7 +531,7 @@ int pa_decode_fp8(const void *q, const void *k_cache, const void *v_cache, const
  * (exact where the scale is a power of two and the value a normal number of
  * that type, saturating at fp16's largest value otherwise), products and sums
  * are fp32, softmax weights are rounded to the storage type.  Calls of few new
- * tokens per sequence (max_query_len up to 16) run on pa_decode_fp8's kernels
+ * tokens per sequence (max_query_len up to 24) run on pa_decode_fp8's kernels
  * and arithmetic instead.  Any finite `scale`.  A NaN among the values of a sequence's live tokens may reach all
  * of its rows in the call.
  *   workspace   device scratch of pa_prefill_fp8_workspace_size bytes,

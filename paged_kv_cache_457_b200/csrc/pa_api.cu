@@ -668,17 +668,9 @@ int append_fp8(pa::AppendArgs &a, int head_dim, int dtype, bool rope, bool inter
 
 // ---- decode over 8-bit caches (pa_fp8.cuh)
 
-// Launch shape of the 8-bit split kernel; overridable at build time for tuning sweeps.
-#ifndef PA_WARPS8
-#define PA_WARPS8 4
-#endif
-#ifndef PA_STAGES8
-#define PA_STAGES8 2
-#endif
-#ifndef PA_BLOCKS8
-#define PA_BLOCKS8 3
-#endif
-constexpr int kWarps8 = PA_WARPS8, kStages8 = PA_STAGES8, kBlocks8 = PA_BLOCKS8;
+// Launch shape of the 8-bit split kernel: 12 warps of two 8 KB slots on an SM.  Measured on 64 sequences of 32 heads: 109
+// us; 8 warps of three slots 125, 16 warps of two (128 registers) 120.
+constexpr int kWarps8 = 4, kStages8 = 2, kBlocks8 = 3;
 static_assert(kWarps8 == kWarps, "blocks_per_sm sizes blocks with kWarps warps");
 
 // Query heads handled together: the largest divisor of the group not above 8 (the mma's columns); one kernel serves
@@ -717,11 +709,15 @@ const void *segment8_kernel_for(int dtype, int head_dim) {
 uint32_t segment8_smem(int head_dim) {
   return head_dim == 128 ? pa::SegSmem8<128, kWarps8>::BYTES : pa::SegSmem8<64, kWarps8>::BYTES;
 }
-// Units of at most this many tiles may take the per-unit kernel (kWarps8 warps x 4).
-#ifndef PA_SEG8_TILES
-#define PA_SEG8_TILES 64
-#endif
-constexpr int kSegmentMaxTiles8 = PA_SEG8_TILES;
+// Whether `units` units of up to max_tiles tiles go to the per-unit kernel, given that they fit one wave of its blocks.
+// A warp takes about 1 us per tile on either path: max_tiles / kWarps8 of them there, its share of all tiles in the
+// split kernel, whose tile prefix, queue and merge cost about 12 us more.  Measured, per-unit against split: 5.5 / 12.4
+// us for 1 sequence of 200 tokens and 8 kv heads, 12.0 / 13.0 for 1000, 20.3 / 16.2 for 2000; 21.1 / 24.0 for 13 of
+// 2000, 39.5 / 33.0 for 13 of 4000; 41.4 / 48.1 for 13 of 2000 with 32 kv heads.
+bool small_units8(long long units, long long max_tiles, int sms) {
+  const long long wave = (long long)sms * kBlocks8 * kWarps8;
+  return max_tiles <= 128 && max_tiles * wave <= kWarps8 * (12 * wave + units * max_tiles);
+}
 
 // As plan_decode, on tiles of pa::TILE8 tokens; num_groups row groups of `columns` columns per unit, HC units each.
 template <bool FEW>
@@ -733,7 +729,7 @@ int plan_decode8(long long num_groups, int columns, int HC, int head_dim, long l
   if (rc != PA_OK) return rc;
   const long long max_tiles = (max_context_len + pa::TILE8 - 1) / pa::TILE8;
   lp->segment_mode = false;
-  if (partition_tokens == 0 && max_tiles <= kSegmentMaxTiles8) {
+  if (partition_tokens == 0 && small_units8(num_groups * HC, max_tiles, sms)) {
     lp->smem = segment8_smem(head_dim);
     int o16 = 0, o_bf = 0;
     if ((rc = blocks_per_sm(segment8_kernel_for<FEW>(PA_FLOAT16, head_dim), lp->smem, &o16)) != PA_OK) return rc;
@@ -842,10 +838,12 @@ int run_decode8(pa::Decode8Args &args, const LaunchPlan &lp, int head_dim, int d
 }
 
 // A prefill call of few tokens per sequence runs on the decode kernels, a row group per tokens that fill the eight
-// columns; more go to the 128-row tiles of prefill8_tc_kernel.
-#ifndef PA_FEW_TOKENS8
-#define PA_FEW_TOKENS8 16
-#endif
+// columns; more go to the 128-row tiles of prefill8_tc_kernel, whose time hardly depends on the tokens while a tile holds
+// them.  Measured, this against those: 64 sequences of up to 2000 tokens, 32 q / 8 kv heads, 8 / 16 / 24 / 32 tokens each
+// 126 / 229 / 330 / 434 against 376 / 379 / 380 / 383 us, with 32 kv heads 132 / 231 / 332 / 438 against 375 to 382; 4 of
+// up to 16000 tokens 71 / 132 / 181 / 230 against 256.  Many row groups keep to those tiles too: every block of the split
+// kernel walks all of their lengths.
+constexpr int kFewTokens8 = 24, kFewGroups8 = 4096;
 struct FewTokens {
   bool use;
   int tokens, groups, columns, HC;
@@ -859,7 +857,7 @@ FewTokens few_tokens(int num_seqs, int num_q_heads, int num_kv_heads, int max_qu
   f.columns = f.tokens * G;
   f.HC = num_kv_heads * (group / G);
   f.num_groups = (long long)num_seqs * f.groups;
-  f.use = max_query_len <= PA_FEW_TOKENS8 && f.num_groups <= 4096;
+  f.use = max_query_len <= kFewTokens8 && f.num_groups <= kFewGroups8;
   return f;
 }
 

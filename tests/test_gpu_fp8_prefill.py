@@ -66,7 +66,7 @@ def test_matches_reference(dtype, hq, hkv, d, bs, case):
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
-@pytest.mark.parametrize("new", [1, 2, 5, 16, 17, 40])
+@pytest.mark.parametrize("new", [1, 2, 5, 16, 17, 24, 25, 40])
 def test_few_tokens_behind_long_contexts(dtype, new):
     require_gpu()
     rng = np.random.default_rng(new)
