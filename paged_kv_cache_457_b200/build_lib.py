@@ -37,7 +37,8 @@ def command(out: str = LIB, verbose_ptxas: bool = False, debug: bool = False) ->
     cmd = [nvcc(), "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
            "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-o", out] + SOURCES
     if debug:
-        cmd[1:1] = ["-DPA_DEBUG"]
+        # optimised on all cores, which the release build is not: it changes the kernels' code
+        cmd[1:1] = ["-DPA_DEBUG", "--split-compile=0"]
     if verbose_ptxas:
         cmd[1:1] = ["-Xptxas", "-v"]
     return cmd

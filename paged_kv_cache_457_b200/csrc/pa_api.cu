@@ -574,6 +574,7 @@ int check_append(const pa::AppendArgs &a, int head_dim, int dtype, bool rope, bo
   if (rope && (!aligned16(a.cos_sin) || (reinterpret_cast<uintptr_t>(a.positions) & 7u))) return PA_ERR_ALIGN;
   if (a.num_q_heads > 0 && (!aligned16(a.q) || !aligned16(a.q_out) || a.q_stride % 8 || a.q_out_stride % 8))
     return PA_ERR_ALIGN;
+  if (a.num_q_heads > 0 && a.q == a.q_out && a.q_stride != a.q_out_stride) return PA_ERR_SHAPE;  // not in place
   if (fp8 && ((reinterpret_cast<uintptr_t>(a.k_scale) | reinterpret_cast<uintptr_t>(a.v_scale)) & 3u))
     return PA_ERR_ALIGN;
   return PA_OK;

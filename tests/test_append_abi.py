@@ -33,6 +33,7 @@ def test_rope_refusals(lib, call):
                        (dict(maxp=0), -3), (dict(hkv=1 << 20), -3), (dict(k=None), -1), (dict(sm=None), -1),
                        (dict(pos=None), -1), (dict(cs=None), -1), (dict(q=None), -1), (dict(qo=None), -1),
                        (dict(ks=128), -3), (dict(vs=128), -3), (dict(qs=256), -3), (dict(qos=256), -3),
+                       (dict(qs=1024), -3),  # q_out is q with another stride
                        (dict(q=24), -4), (dict(k=24), -4), (dict(kc=24), -4), (dict(qs=516), -4), (dict(ks=260), -4),
                        (dict(pos=20), -4), (dict(sm=20), -4), (dict(cs=24), -4)):
         assert call(lib, **over) == code, over
