@@ -15,6 +15,8 @@ CPU fallback: if the library is missing or no GPU is present the calls raise.
 * :func:`rope_write_kv` -- the write with the rotary position embedding applied on the way;
   :func:`write_kv_fp8`, :func:`rope_write_kv_fp8` -- into caches held in 8 bits with a
   scale for each block and kv head.
+* :func:`decode_fp8`, :func:`prefill_fp8` -- attention over such caches;
+  :func:`copy_blocks_fp8`, :func:`swap_blocks_fp8` -- their block copies.
 
 Caches are ``[num_blocks, num_kv_heads, block_size, head_dim]`` float16 or
 bfloat16 tensors; ``block_tables`` int32 ``[S, max_blocks]``; ``context_lens``

@@ -12,10 +12,13 @@ a tensor once and build their messages only when one fails.
 from __future__ import annotations
 
 import ctypes
+import sys
 
 import torch
 
 from . import PagedAttentionError, _DTYPES, _cache_geometry, _check, _need_cuda, load_library
+
+_package = sys.modules[__package__]
 
 F8 = torch.float8_e4m3fn
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
@@ -34,9 +37,16 @@ def bind(lib: ctypes.CDLL) -> None:
         f.argtypes = args
 
 
+def library() -> ctypes.CDLL:
+    """The loaded library (loading it takes a lock, which a call need not)."""
+    return _package._lib or load_library()
+
+
 def stream_of(dev: torch.device) -> int:
     """The current stream of ``dev`` as the C ABI takes it."""
-    return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    if _raw_stream is None or dev.index is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev.index)
 
 
 def on_device(dev: torch.device, f, *args) -> int:
@@ -154,12 +164,15 @@ def rope_write_kv(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_ca
     if dev is None:
         need_cuda(k_cache=k_cache, k=k, v=v, v_cache=v_cache, slot_mapping=slot_mapping,
                   positions=positions, cos_sin=cos_sin, q=q, q_out=q_out)
-    nb, hkv, bs, d = _cache_geometry(k_cache, v_cache)
-    dtype = k_cache.dtype
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape or dtype not in _DTYPES or v_cache.dtype is not dtype \
+            or not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        _cache_geometry(k_cache, v_cache)  # says what is wrong
+    nb, hkv, bs, d = shape
     T = _tokens(slot_mapping)
     ks, vs = token_stride("k", k, T, hkv, d, dtype), token_stride("v", v, T, hkv, d, dtype)
     qp, q_out, qop, hq, qs, qos, rot, maxp = _rope_args(q, q_out, T, d, dtype, positions, cos_sin, dev)
-    rc = on_device(dev, load_library().pa_rope_write_kv, qp, k.data_ptr(), v.data_ptr(), qop, k_cache.data_ptr(),
+    rc = on_device(dev, library().pa_rope_write_kv, qp, k.data_ptr(), v.data_ptr(), qop, k_cache.data_ptr(),
                    v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), T, hq, hkv, d,
                    rot, 1 if interleaved else 0, bs, nb, maxp, qs, ks, vs, qos, _DTYPES[dtype], stream_of(dev))
     if rc:
@@ -185,7 +198,7 @@ def write_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
         raise PagedAttentionError("k and v must be float16 or bfloat16")
     T = _tokens(slot_mapping)
     ks, vs = token_stride("k", k, T, hkv, d, dtype), token_stride("v", v, T, hkv, d, dtype)
-    rc = on_device(dev, load_library().pa_write_kv_fp8, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+    rc = on_device(dev, library().pa_write_kv_fp8, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
                    v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), slot_mapping.data_ptr(), T, hkv, d, bs,
                    nb, ks, vs, _DTYPES[dtype], stream_of(dev))
     if rc:
@@ -209,7 +222,7 @@ def rope_write_kv_fp8(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, 
     T = _tokens(slot_mapping)
     ks, vs = token_stride("k", k, T, hkv, d, dtype), token_stride("v", v, T, hkv, d, dtype)
     qp, q_out, qop, hq, qs, qos, rot, maxp = _rope_args(q, q_out, T, d, dtype, positions, cos_sin, dev)
-    rc = on_device(dev, load_library().pa_rope_write_kv_fp8, qp, k.data_ptr(), v.data_ptr(), qop, k_cache.data_ptr(),
+    rc = on_device(dev, library().pa_rope_write_kv_fp8, qp, k.data_ptr(), v.data_ptr(), qop, k_cache.data_ptr(),
                    v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), slot_mapping.data_ptr(),
                    positions.data_ptr(), cos_sin.data_ptr(), T, hq, hkv, d, rot, 1 if interleaved else 0, bs, nb, maxp,
                    qs, ks, vs, qos, _DTYPES[dtype], stream_of(dev))

@@ -8,9 +8,8 @@ import ctypes
 
 import torch
 
-from . import (PagedAttentionError, _DTYPES, _check, _mapping, _need_cuda, _workspace, _workspaces,
-               load_library)
-from .append import fp8_geometry, need_cuda, on_device, same_device, stream_of, token_stride
+from . import PagedAttentionError, _DTYPES, _check, _mapping, _need_cuda, _workspace, _workspaces
+from .append import fp8_geometry, library, need_cuda, on_device, same_device, stream_of, token_stride
 
 PA_ERR_WORKSPACE = -7
 
@@ -74,7 +73,7 @@ def _run(dev, what, size, call, workspace):
 def decode_fp8_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
                               partition_tokens: int = 0) -> int:
     """Device workspace bytes of :func:`decode_fp8` for these sizes on the current device (0: none, or bad input)."""
-    return int(load_library().pa_decode_fp8_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+    return int(library().pa_decode_fp8_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                                                            max_context_len, partition_tokens))
 
 
@@ -104,7 +103,7 @@ def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
     if max_context_len is None:
         max_context_len = context_lens.max().item() if S else 0
     max_context_len, partition_tokens, scale = int(max_context_len), int(partition_tokens), float(scale)
-    lib = load_library()
+    lib = library()
 
     def call(ws, nbytes, stream):
         return lib.pa_decode_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
@@ -146,7 +145,7 @@ def prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k
         _need_cuda("out", out, dev)
         os_ = token_stride("out", out, N, hq, d, dtype)
     max_query_len, scale = int(max_query_len), float(scale)
-    lib = load_library()
+    lib = library()
 
     def call(ws, nbytes, stream):
         return lib.pa_prefill_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
@@ -168,7 +167,7 @@ def copy_blocks_fp8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch
     dev = k_cache.device
     nb, hkv, bs, d = fp8_geometry(k_cache, v_cache, k_scale, v_scale)
     m = _mapping(block_mapping, dev)
-    rc = on_device(dev, load_library().pa_copy_blocks_fp8, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+    rc = on_device(dev, library().pa_copy_blocks_fp8, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                    v_scale.data_ptr(), m.data_ptr(), m.shape[0], hkv, d, bs, nb, stream_of(dev))
     _check(rc, "pa_copy_blocks_fp8")
 
@@ -187,6 +186,6 @@ def swap_blocks_fp8(src_k: torch.Tensor, src_v: torch.Tensor, src_k_scale: torch
     if tuple(rest) != (hkv, bs, d):
         raise PagedAttentionError("pools must share heads, block size and head dim")
     m = _mapping(block_mapping, dev)
-    rc = on_device(dev, load_library().pa_swap_blocks_fp8, *(t.data_ptr() for t in pools), m.data_ptr(), m.shape[0], hkv,
+    rc = on_device(dev, library().pa_swap_blocks_fp8, *(t.data_ptr() for t in pools), m.data_ptr(), m.shape[0], hkv,
                    d, bs, snb, dnb, stream_of(dev))
     _check(rc, "pa_swap_blocks_fp8")

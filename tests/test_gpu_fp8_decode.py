@@ -104,6 +104,38 @@ def test_query_magnitudes(gain):
     check(out, q, b, "bf16", float(np.float32(0.0883)))
 
 
+@pytest.mark.parametrize("part", [0, 64])
+@pytest.mark.parametrize("scale", [-0.1, 0.0])
+def test_any_finite_scale_and_a_nan_row(scale, part):
+    require_gpu()
+    rng = np.random.default_rng(26)
+    b = Batch(rng, [200, 77, 31], 2, 64, 16)
+    q = queries(rng, "bf16", 3, 4, 64)
+    kc, vc, ks, vs = on_gpu(b)
+    call = lambda x: pa.decode_fp8(x.cuda(), kc, vc, ks, vs, dev(b.tables), dev(b.ctx), scale, 200, partition_tokens=part)  # noqa: E731
+    good = call(q)
+    check(good, q, b, "bf16", float(np.float32(scale)))
+    q[1, 2] = float("nan")
+    out = call(q)
+    same = torch.ones(3, 4, dtype=torch.bool, device="cuda")
+    same[1, 2] = False
+    assert torch.equal(out[same], good[same]) and torch.isnan(out[1, 2]).all()
+
+
+def test_tables_cut_from_wider_ones():
+    require_gpu()
+    rng = np.random.default_rng(27)
+    b = Batch(rng, [100, 0, 64], 2, 64, 16, width=13)
+    q = queries(rng, "fp16", 3, 4, 64)
+    kc, vc, ks, vs = on_gpu(b)
+    t = dev(b.tables)
+    want = pa.decode_fp8(q.cuda(), kc, vc, ks, vs, t, dev(b.ctx), 0.125, 100)
+    assert torch.equal(pa.decode_fp8(q.cuda(), kc, vc, ks, vs, t[:, :7], dev(b.ctx), 0.125, 100), want)
+    one = pa.decode_fp8(q.cuda()[:1], kc, vc, ks, vs, t[:1, :7], dev(b.ctx[:1]), 0.125, 100)
+    assert torch.equal(one, want[:1])
+    check(want, q, b, "fp16", 0.125)
+
+
 def test_sharp_weights_and_a_rising_maximum():
     """Keys that raise the maximum again and again, and one token that takes all the weight."""
     require_gpu()

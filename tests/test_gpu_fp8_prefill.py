@@ -80,6 +80,41 @@ def test_few_tokens_behind_long_contexts(dtype, new):
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("hq,hkv,d,bs", [(7, 1, 128, 16), (3, 3, 64, 32), (16, 1, 64, 16), (5, 5, 128, 32), (11, 1, 128, 16),
+                                         (12, 2, 64, 16), (32, 4, 128, 16)])
+@pytest.mark.parametrize("ctx0", [0, 90, 1500])
+def test_few_tokens_of_every_grouping(dtype, hq, hkv, d, bs, ctx0):
+    """Row groups of one to eight tokens; tables wide enough for the split kernel, and narrow ones for the other."""
+    require_gpu()
+    rng = np.random.default_rng(hq + ctx0)
+    new = [9, 1, 0, 4, 7, 2]
+    b = Batch(rng, [n + ctx0 + i * 17 if n else 40 for i, n in enumerate(new)], hkv, d, bs, width=500 if ctx0 else None)
+    q = queries(rng, dtype, sum(new), hq, d)
+    out = run(b, q, new, d ** -0.5)
+    check(out, q, b, new, dtype, d ** -0.5)
+    assert pa.device_status() == 0
+
+
+@pytest.mark.parametrize("new", [[6, 3], [150, 40]])
+def test_nan_stays_its_own(new):
+    """A query row of NaN, and a sequence whose values are NaN: the other rows are as before."""
+    require_gpu()
+    rng = np.random.default_rng(38)
+    b = Batch(rng, [n + 50 for n in new], 2, 64, 16)
+    q = queries(rng, "bf16", sum(new), 4, 64)
+    good = run(b, q, new, 0.125)
+    q2 = q.clone()
+    q2[1, 2] = float("nan")
+    out = run(b, q2, new, 0.125)
+    same = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+    same[1, 2] = False
+    assert torch.equal(out[same], good[same]) and torch.isnan(out[1, 2]).all()
+    b.pools[2][b.tables[1, 0]] = 0x7F
+    out = run(b, q, new, 0.125)
+    assert torch.equal(out[:new[0]], good[:new[0]]) and torch.isnan(out[new[0]:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("new", [[6, 3], [150, 40]])
 def test_scales_that_are_no_powers_of_two(dtype, new):
     require_gpu()
