@@ -242,216 +242,218 @@ __global__ void __launch_bounds__(PF8_THREADS, 1)
     return ok;
   };
 
-  if (warp >= 8 && warp != 10) {
-    // ------------------------------------------------------------ loaders (warp 8 also takes the items and loads Q)
+  // One instruction per warpgroup (8-11 and 12-15 give, 0-3 and 4-7 take), all of its warps together.
+  if (warp >= 8) {
     give_registers<PF8_OTHER_REGS>();
-    const int w = warp > 10 ? warp - 9 : warp - 8;
-    if (w == 0 && lane == 0) prefetch_tensor_map(&tmap_q);
-    long long g = 0;  // K/V tiles of the items before
-    int n_items = 0;
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      long long item;
-      PrefillItem it;
-      if (w == 0) {
-        // the next item with work; items whose rows, context or pages are invalid are settled here
-        const int slot = k & 3;
-        if (k >= 4 && !(ok = warp_wait(&item_empty[slot], (uint32_t)(((k >> 2) - 1) & 1), limit))) break;
-        for (;;) {
-          unsigned int t = 0;
-          if (lane == 0) t = atomicAdd(a.queue, 1u);
-          item = (long long)__shfl_sync(FULL, t, 0);
-          if (item >= a.num_items) {
-            item = -1;
-            break;
-          }
-          it = prefill_item(a, item);
-          if (!dcheck(it.s < a.num_seqs && it.hq < a.num_q_heads)) continue;
-          if (it.past_grid && it.t0 == 0 && it.hq == 0 && lane == 0) atomicOr(&g_status, PA_DEV_ERR_CONTEXT_HINT);
-          bool zero = it.bad_ctx;
-          if (it.work) {
-            const int pages = (it.kmax + a.block_size - 1) / a.block_size;
-            const int32_t *row = a.block_tables + (long long)it.s * a.table_stride;
-            bool bad = false;
-#pragma unroll 4
-            for (int p = lane; p < pages; p += 32) {
-              const int blk = __ldg(row + p);
-              bad |= blk < 0 || (long long)blk >= a.num_blocks;
-            }
-            zero = __any_sync(FULL, bad);
-            if (!zero) break;
-          } else if (!zero && lane == 0) {
-            // no rows of this sequence at this query tile (or no valid rows at all): the same holds for the
-            // sequence's remaining heads, which are the next items; move the counter past them
-            atomicMax(a.queue, (unsigned int)(item + a.num_q_heads - it.hq));
-            if (it.bad_rows) atomicOr(&g_status, PA_DEV_ERR_CONTEXT);
-          }
-          if (zero) {  // zero the item's rows
-            if (lane == 0) atomicOr(&g_status, it.bad_ctx ? PA_DEV_ERR_CONTEXT : PA_DEV_ERR_BLOCK_ID);
-            for (int r = lane; r < it.rows; r += 32) {
-              if (!dcheck((long long)it.q0 + it.t0 + r < a.num_query_tokens)) break;
-              uint4 *dst = reinterpret_cast<uint4 *>(a.out + (long long)(it.q0 + it.t0 + r) * a.out_token_stride +
-                                                     (long long)it.hq * D);
-#pragma unroll
-              for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
-            }
-          }
-        }
-        if (lane == 0) {
-          items[slot] = item;
-          mbar_arrive(&item_full[slot]);  // release: the item index is visible to the readers
-        }
-        if (item < 0) break;
-        if (n_items >= 1 && !(ok = warp_wait(q_empty, (uint32_t)((n_items - 1) & 1), limit))) break;
-        if (lane == 0) mbar_arrive_expect_tx(q_full, 2 * PF_BM * D * 2);
-        __syncwarp();
-        if (lane < 2 * HALVES) {  // lane = sub-tile * HALVES + half
-          const int x = lane / HALVES, hh = lane % HALVES;
-          tc::tma_load_3d(sm + L::Q + lane * REGION, &tmap_q, hh * 64, it.hq, it.q0 + it.t0 + x * PF_BM, q_full);
-        }
-      } else {
-        if (!(ok = take_item(k, true, &item))) break;
-        if (item < 0) break;
-        it = prefill_item(a, item);
-      }
-      // The item's units: per key tile four of K, then four of V; unit number modulo PF8_LOADERS names the warp.
-      const int32_t *row = a.block_tables + (long long)it.s * a.table_stride;
-      const int pages = (it.kmax + a.block_size - 1) / a.block_size;
-      int win = -1, ent = -1, ent_next = -1;  // 32 table entries from page 32 win on, and the 32 after them
-      auto entries = [&](int wi) {
-        return wi * 32 + lane < pages && dcheck(pages <= a.table_stride) ? __ldg(row + wi * 32 + lane) : -1;
-      };
-      auto load = [&](int u, LoadUnit<E, D> &x) {
-        const int tok0 = (u >> 3) * PF_BN + (u & 3) * 32;
-        const int page = tok0 / a.block_size, wi = page >> 5;
-        if (wi != win) {
-          ent = wi == win + 1 && win >= 0 ? ent_next : entries(wi);
-          win = wi;
-          ent_next = entries(wi + 1);
-        }
-        const int p0 = __shfl_sync(FULL, ent, page & 31);
-        const int p1 = a.block_size == 16 ? __shfl_sync(FULL, ent, (page + 1) & 31) : p0;
-        const bool is_v = (u >> 2) & 1;
-        x.load(is_v ? args.v_cache : args.k_cache, is_v ? args.v_scale : args.k_scale, a, it.h, p0, p1, tok0, it.kmax,
-               lane);
-      };
-      const int units = it.nt * 8;
-      const int u0 = (int)((w + PF8_LOADERS - (g * 8) % PF8_LOADERS) % PF8_LOADERS);
-      LoadUnit<E, D> x;
-      for (int u = u0; u < units; u += PF8_LOADERS) {
-        load(u, x);  // in flight while the slot is waited for
-        const long long t = g + (u >> 3);
-        const bool is_v = (u >> 2) & 1;
-        const int nst = is_v ? PF8_VST : PF8_KST;
-        const int st = (int)(t % nst);
-        if (t >= nst && !(ok = warp_wait(&(is_v ? v_empty : k_empty)[st], (uint32_t)(((t / nst) - 1) & 1), limit))) break;
-        if (__any_sync(FULL, *abort_flag != 0)) {
-          ok = false;
-          break;
-        }
-        x.store(sm + (is_v ? L::V : L::K) + st * HALVES * REGION, (u & 3) * 32, is_v ? 1.f : args.k_sign, lane);
-        fence_proxy_async_smem();  // the tensor cores read the rows through the async proxy
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&(is_v ? v_full : k_full)[st]);
-      }
-      g += it.nt;
-      ++n_items;
-    }
-    if (!ok && lane == 0) {
-      *abort_flag = 1;
-      atomicOr(&g_status, PA_DEV_ERR_TIMEOUT);
-    }
-    // Q's copies have landed before the CTA's smem is given back
-    if (w == 0 && n_items > 0 && !warp_wait(q_full, (uint32_t)((n_items - 1) & 1), limit) && lane == 0)
-      atomicOr(&g_status, PA_DEV_ERR_TIMEOUT);
-  } else if (warp == 10) {
-    // ------------------------------------------------------------ MMA issue (one lane)
-    give_registers<PF8_OTHER_REGS>();
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = tc::idesc_f16(kBf16, false, PF_BM, PF_BN);
-      constexpr uint32_t idesc_pv = tc::idesc_f16(kBf16, true, PF_BM, D);
-      const uint32_t qs = sbase + L::Q;
-      long long g = 0;           // K/V tiles
-      long long gx[2] = {0, 0};  // tiles of sub-tile A, B
+    if (warp != 10) {
+      // ------------------------------------------------------------ loaders (warp 8 also takes the items and loads Q)
+      const int w = warp > 10 ? warp - 9 : warp - 8;
+      if (w == 0 && lane == 0) prefetch_tensor_map(&tmap_q);
+      long long g = 0;  // K/V tiles of the items before
       int n_items = 0;
       bool ok = true;
-      // S_x = Q_x K(t)^T
-      auto issue_qk = [&](int x, long long t) {
-        const uint32_t ks = sbase + L::K + (uint32_t)(t % PF8_KST) * HALVES * REGION;
-        const uint32_t qx = qs + x * HALVES * REGION;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * REGION + (k % 4) * 32;
-          tc::mma_ss(tmem + L::T_S + x * 128, tc::desc_sw128(qx + off, 16, 1024), tc::desc_sw128(ks + off, 16, 1024),
-                     idesc_qk, k > 0);
-        }
-        tc::commit(&s_full[x]);
-      };
-      // O_x += P_x V(t), once softmax_x has written P_x for its tile gx
-      auto issue_pv = [&](int x, long long t, long long tx, bool first_of_item) -> bool {
-        if (!mbar_wait_bounded(&p_full[x], (uint32_t)(tx & 1), limit)) return false;
-        const int st = (int)(t % PF8_VST);
-        if (!mbar_wait_bounded(&v_full[st], (uint32_t)((t / PF8_VST) & 1), limit)) return false;
-        tc::fence_after_sync();
-        const uint32_t vs = sbase + L::V + st * HALVES * REGION;
-#pragma unroll
-        for (int k = 0; k < PF_BN / 16; ++k)
-          tc::mma_ts(tmem + L::T_O + x * D, tmem + L::T_S + x * 128 + k * 8,
-                     tc::desc_sw128(vs + k * 16 * 128, REGION, 1024), idesc_pv, !first_of_item || k > 0);
-        return true;
-      };
       for (int k = 0; ok; ++k) {
         long long item;
-        if (!(ok = take_item(k, false, &item))) break;
-        if (item < 0) break;
-        const PrefillItem it = prefill_item(a, item);
-        if (!(ok = mbar_wait_bounded(q_full, (uint32_t)(n_items & 1), limit))) break;
-        long long pend_t = -1, pend_tb = 0;  // PV_B due next: K/V tile and B's tile
-        bool pend_first = false;
-        for (int j = 0; j < it.nt; ++j, ++g) {
-          if (*abort_flag) {
+        PrefillItem it;
+        if (w == 0) {
+          // the next item with work; items whose rows, context or pages are invalid are settled here
+          const int slot = k & 3;
+          if (k >= 4 && !(ok = warp_wait(&item_empty[slot], (uint32_t)(((k >> 2) - 1) & 1), limit))) break;
+          for (;;) {
+            unsigned int t = 0;
+            if (lane == 0) t = atomicAdd(a.queue, 1u);
+            item = (long long)__shfl_sync(FULL, t, 0);
+            if (item >= a.num_items) {
+              item = -1;
+              break;
+            }
+            it = prefill_item(a, item);
+            if (!dcheck(it.s < a.num_seqs && it.hq < a.num_q_heads)) continue;
+            if (it.past_grid && it.t0 == 0 && it.hq == 0 && lane == 0) atomicOr(&g_status, PA_DEV_ERR_CONTEXT_HINT);
+            bool zero = it.bad_ctx;
+            if (it.work) {
+              const int pages = (it.kmax + a.block_size - 1) / a.block_size;
+              const int32_t *row = a.block_tables + (long long)it.s * a.table_stride;
+              bool bad = false;
+#pragma unroll 4
+              for (int p = lane; p < pages; p += 32) {
+                const int blk = __ldg(row + p);
+                bad |= blk < 0 || (long long)blk >= a.num_blocks;
+              }
+              zero = __any_sync(FULL, bad);
+              if (!zero) break;
+            } else if (!zero && lane == 0) {
+              // no rows of this sequence at this query tile (or no valid rows at all): the same holds for the
+              // sequence's remaining heads, which are the next items; move the counter past them
+              atomicMax(a.queue, (unsigned int)(item + a.num_q_heads - it.hq));
+              if (it.bad_rows) atomicOr(&g_status, PA_DEV_ERR_CONTEXT);
+            }
+            if (zero) {  // zero the item's rows
+              if (lane == 0) atomicOr(&g_status, it.bad_ctx ? PA_DEV_ERR_CONTEXT : PA_DEV_ERR_BLOCK_ID);
+              for (int r = lane; r < it.rows; r += 32) {
+                if (!dcheck((long long)it.q0 + it.t0 + r < a.num_query_tokens)) break;
+                uint4 *dst = reinterpret_cast<uint4 *>(a.out + (long long)(it.q0 + it.t0 + r) * a.out_token_stride +
+                                                       (long long)it.hq * D);
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
+              }
+            }
+          }
+          if (lane == 0) {
+            items[slot] = item;
+            mbar_arrive(&item_full[slot]);  // release: the item index is visible to the readers
+          }
+          if (item < 0) break;
+          if (n_items >= 1 && !(ok = warp_wait(q_empty, (uint32_t)((n_items - 1) & 1), limit))) break;
+          if (lane == 0) mbar_arrive_expect_tx(q_full, 2 * PF_BM * D * 2);
+          __syncwarp();
+          if (lane < 2 * HALVES) {  // lane = sub-tile * HALVES + half
+            const int x = lane / HALVES, hh = lane % HALVES;
+            tc::tma_load_3d(sm + L::Q + lane * REGION, &tmap_q, hh * 64, it.hq, it.q0 + it.t0 + x * PF_BM, q_full);
+          }
+        } else {
+          if (!(ok = take_item(k, true, &item))) break;
+          if (item < 0) break;
+          it = prefill_item(a, item);
+        }
+        // The item's units: per key tile four of K, then four of V; unit number modulo PF8_LOADERS names the warp.
+        const int32_t *row = a.block_tables + (long long)it.s * a.table_stride;
+        const int pages = (it.kmax + a.block_size - 1) / a.block_size;
+        int win = -1, ent = -1, ent_next = -1;  // 32 table entries from page 32 win on, and the 32 after them
+        auto entries = [&](int wi) {
+          return wi * 32 + lane < pages && dcheck(pages <= a.table_stride) ? __ldg(row + wi * 32 + lane) : -1;
+        };
+        auto load = [&](int u, LoadUnit<E, D> &x) {
+          const int tok0 = (u >> 3) * PF_BN + (u & 3) * 32;
+          const int page = tok0 / a.block_size, wi = page >> 5;
+          if (wi != win) {
+            ent = wi == win + 1 && win >= 0 ? ent_next : entries(wi);
+            win = wi;
+            ent_next = entries(wi + 1);
+          }
+          const int p0 = __shfl_sync(FULL, ent, page & 31);
+          const int p1 = a.block_size == 16 ? __shfl_sync(FULL, ent, (page + 1) & 31) : p0;
+          const bool is_v = (u >> 2) & 1;
+          x.load(is_v ? args.v_cache : args.k_cache, is_v ? args.v_scale : args.k_scale, a, it.h, p0, p1, tok0, it.kmax,
+                 lane);
+        };
+        const int units = it.nt * 8;
+        const int u0 = (int)((w + PF8_LOADERS - (g * 8) % PF8_LOADERS) % PF8_LOADERS);
+        LoadUnit<E, D> x;
+        for (int u = u0; u < units; u += PF8_LOADERS) {
+          load(u, x);  // in flight while the slot is waited for
+          const long long t = g + (u >> 3);
+          const bool is_v = (u >> 2) & 1;
+          const int nst = is_v ? PF8_VST : PF8_KST;
+          const int st = (int)(t % nst);
+          if (t >= nst && !(ok = warp_wait(&(is_v ? v_empty : k_empty)[st], (uint32_t)(((t / nst) - 1) & 1), limit))) break;
+          if (__any_sync(FULL, *abort_flag != 0)) {
             ok = false;
             break;
           }
-          const bool a_on = j < it.nt_a, b_on = it.has_b;
-          if (!(ok = mbar_wait_bounded(&k_full[g % PF8_KST], (uint32_t)((g / PF8_KST) & 1), limit))) break;
-          tc::fence_after_sync();
-          if (a_on) issue_qk(0, g);
-          if (pend_t >= 0) {
-            if (!(ok = issue_pv(1, pend_t, pend_tb, pend_first))) break;
-            tc::commit(&v_empty[pend_t % PF8_VST]);
-            pend_t = -1;
-          }
-          if (b_on) issue_qk(1, g);
-          tc::commit(&k_empty[g % PF8_KST]);
-          if (j == it.nt - 1) tc::commit(q_empty);
-          if (a_on) {
-            if (!(ok = issue_pv(0, g, gx[0], j == 0))) break;
-            if (j == it.nt_a - 1) tc::commit(&o_done[0]);
-            if (!b_on) tc::commit(&v_empty[g % PF8_VST]);
-            ++gx[0];
-          }
-          if (b_on) {
-            pend_t = g;
-            pend_tb = gx[1]++;
-            pend_first = j == 0;
-          }
+          x.store(sm + (is_v ? L::V : L::K) + st * HALVES * REGION, (u & 3) * 32, is_v ? 1.f : args.k_sign, lane);
+          fence_proxy_async_smem();  // the tensor cores read the rows through the async proxy
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&(is_v ? v_full : k_full)[st]);
         }
-        if (ok && pend_t >= 0) {  // the item's last PV_B
-          if ((ok = issue_pv(1, pend_t, pend_tb, pend_first))) {
-            tc::commit(&v_empty[pend_t % PF8_VST]);
-            tc::commit(&o_done[1]);
-          }
-        }
+        g += it.nt;
         ++n_items;
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         *abort_flag = 1;
         atomicOr(&g_status, PA_DEV_ERR_TIMEOUT);
       }
-      // Every MMA issued has finished before tensor memory and smem are released.
-      tc::commit(drained);
-      if (!mbar_wait_bounded(drained, 0, limit)) atomicOr(&g_status, PA_DEV_ERR_TIMEOUT);
+      // Q's copies have landed before the CTA's smem is given back
+      if (w == 0 && n_items > 0 && !warp_wait(q_full, (uint32_t)((n_items - 1) & 1), limit) && lane == 0)
+        atomicOr(&g_status, PA_DEV_ERR_TIMEOUT);
+    } else {
+      // ------------------------------------------------------------ MMA issue (one lane)
+      if (lane == 0) {
+        constexpr uint32_t idesc_qk = tc::idesc_f16(kBf16, false, PF_BM, PF_BN);
+        constexpr uint32_t idesc_pv = tc::idesc_f16(kBf16, true, PF_BM, D);
+        const uint32_t qs = sbase + L::Q;
+        long long g = 0;           // K/V tiles
+        long long gx[2] = {0, 0};  // tiles of sub-tile A, B
+        int n_items = 0;
+        bool ok = true;
+        // S_x = Q_x K(t)^T
+        auto issue_qk = [&](int x, long long t) {
+          const uint32_t ks = sbase + L::K + (uint32_t)(t % PF8_KST) * HALVES * REGION;
+          const uint32_t qx = qs + x * HALVES * REGION;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * REGION + (k % 4) * 32;
+            tc::mma_ss(tmem + L::T_S + x * 128, tc::desc_sw128(qx + off, 16, 1024), tc::desc_sw128(ks + off, 16, 1024),
+                       idesc_qk, k > 0);
+          }
+          tc::commit(&s_full[x]);
+        };
+        // O_x += P_x V(t), once softmax_x has written P_x for its tile gx
+        auto issue_pv = [&](int x, long long t, long long tx, bool first_of_item) -> bool {
+          if (!mbar_wait_bounded(&p_full[x], (uint32_t)(tx & 1), limit)) return false;
+          const int st = (int)(t % PF8_VST);
+          if (!mbar_wait_bounded(&v_full[st], (uint32_t)((t / PF8_VST) & 1), limit)) return false;
+          tc::fence_after_sync();
+          const uint32_t vs = sbase + L::V + st * HALVES * REGION;
+#pragma unroll
+          for (int k = 0; k < PF_BN / 16; ++k)
+            tc::mma_ts(tmem + L::T_O + x * D, tmem + L::T_S + x * 128 + k * 8,
+                       tc::desc_sw128(vs + k * 16 * 128, REGION, 1024), idesc_pv, !first_of_item || k > 0);
+          return true;
+        };
+        for (int k = 0; ok; ++k) {
+          long long item;
+          if (!(ok = take_item(k, false, &item))) break;
+          if (item < 0) break;
+          const PrefillItem it = prefill_item(a, item);
+          if (!(ok = mbar_wait_bounded(q_full, (uint32_t)(n_items & 1), limit))) break;
+          long long pend_t = -1, pend_tb = 0;  // PV_B due next: K/V tile and B's tile
+          bool pend_first = false;
+          for (int j = 0; j < it.nt; ++j, ++g) {
+            if (*abort_flag) {
+              ok = false;
+              break;
+            }
+            const bool a_on = j < it.nt_a, b_on = it.has_b;
+            if (!(ok = mbar_wait_bounded(&k_full[g % PF8_KST], (uint32_t)((g / PF8_KST) & 1), limit))) break;
+            tc::fence_after_sync();
+            if (a_on) issue_qk(0, g);
+            if (pend_t >= 0) {
+              if (!(ok = issue_pv(1, pend_t, pend_tb, pend_first))) break;
+              tc::commit(&v_empty[pend_t % PF8_VST]);
+              pend_t = -1;
+            }
+            if (b_on) issue_qk(1, g);
+            tc::commit(&k_empty[g % PF8_KST]);
+            if (j == it.nt - 1) tc::commit(q_empty);
+            if (a_on) {
+              if (!(ok = issue_pv(0, g, gx[0], j == 0))) break;
+              if (j == it.nt_a - 1) tc::commit(&o_done[0]);
+              if (!b_on) tc::commit(&v_empty[g % PF8_VST]);
+              ++gx[0];
+            }
+            if (b_on) {
+              pend_t = g;
+              pend_tb = gx[1]++;
+              pend_first = j == 0;
+            }
+          }
+          if (ok && pend_t >= 0) {  // the item's last PV_B
+            if ((ok = issue_pv(1, pend_t, pend_tb, pend_first))) {
+              tc::commit(&v_empty[pend_t % PF8_VST]);
+              tc::commit(&o_done[1]);
+            }
+          }
+          ++n_items;
+        }
+        if (!ok) {
+          *abort_flag = 1;
+          atomicOr(&g_status, PA_DEV_ERR_TIMEOUT);
+        }
+        // Every MMA issued has finished before tensor memory and smem are released.
+        tc::commit(drained);
+        if (!mbar_wait_bounded(drained, 0, limit)) atomicOr(&g_status, PA_DEV_ERR_TIMEOUT);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax and epilogue of sub-tile x (warps 0-3: A, 4-7: B)
