@@ -47,25 +47,25 @@ def _tables(block_tables: torch.Tensor, context_lens: torch.Tensor, S: int) -> i
     return s0 if S > 1 else max(1, shape[1])
 
 
-def _run(dev, what, size, call, workspace):
-    """call(workspace pointer, bytes, stream) with the caller's workspace, or with one kept per device and stream.
-    A capture gets its own, from the graph's pool: a captured graph may be replayed beside other calls and must
-    neither share theirs nor outlive it."""
+def _run(dev, what, size, sizes, call, args, workspace):
+    """call(*args, workspace pointer, bytes, stream) with the caller's workspace, or with one kept per device and stream
+    (of size(*sizes) bytes).  A capture gets its own, from the graph's pool: a captured graph may be replayed beside
+    other calls and must neither share theirs nor outlive it."""
     stream = stream_of(dev)
     if workspace is not None:
         if workspace.device != dev or not workspace.is_contiguous():
             raise PagedAttentionError("workspace must be a contiguous tensor on the caches' device")
-        rc = call(workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
+        rc = call(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
     elif torch.cuda.is_current_stream_capturing():
-        n = size()
+        n = int(size(*sizes))
         ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        rc = call(ws.data_ptr() if n else None, n, stream)
+        rc = call(*args, ws.data_ptr() if n else None, n, stream)
     else:
         ws = _workspaces.get((dev.index, stream))
-        rc = call(ws.data_ptr(), ws.numel(), stream) if ws is not None else call(None, 0, stream)
+        rc = call(*args, ws.data_ptr(), ws.numel(), stream) if ws is not None else call(*args, None, 0, stream)
         if rc == PA_ERR_WORKSPACE:
-            ws = _workspace(dev, stream, size())
-            rc = call(ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, stream)
+            ws = _workspace(dev, stream, int(size(*sizes)))
+            rc = call(*args, ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, stream)
     if rc:
         _check(rc, what)
 
@@ -95,7 +95,7 @@ def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
     qs = token_stride("q", q, S, hq, d, dtype)
     ts = _tables(block_tables, context_lens, S)
     if out is None:
-        out = torch.empty((S, hq, d), dtype=dtype, device=dev)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty((S, hq, d), dtype=dtype, device=dev)
         os_ = hq * d
     else:
         _need_cuda("out", out, dev)
@@ -105,16 +105,11 @@ def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
     max_context_len, partition_tokens, scale = int(max_context_len), int(partition_tokens), float(scale)
     lib = library()
 
-    def call(ws, nbytes, stream):
-        return lib.pa_decode_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                                 v_scale.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), scale,
-                                 out.data_ptr(), S, hq, hkv, d, bs, nb, ts, max_context_len, qs, os_,
-                                 partition_tokens, _DTYPES[dtype], ws, nbytes, stream)
-
-    def size():
-        return int(lib.pa_decode_fp8_workspace_size(S, hq, hkv, d, bs, max_context_len, partition_tokens))
-
-    on_device(dev, _run, dev, "pa_decode_fp8", size, call, workspace)
+    on_device(dev, _run, dev, "pa_decode_fp8", lib.pa_decode_fp8_workspace_size,
+              (S, hq, hkv, d, bs, max_context_len, partition_tokens), lib.pa_decode_fp8,
+              (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+               block_tables.data_ptr(), context_lens.data_ptr(), scale, out.data_ptr(), S, hq, hkv, d, bs, nb, ts,
+               max_context_len, qs, os_, partition_tokens, _DTYPES[dtype]), workspace)
     return out
 
 
@@ -139,7 +134,7 @@ def prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k
     if query_start.dtype is not torch.int32 or query_start.shape != (S + 1,) or not query_start.is_contiguous():
         raise PagedAttentionError("query_start must be a contiguous int32 [S + 1] tensor")
     if out is None:
-        out = torch.empty((N, hq, d), dtype=dtype, device=dev)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty((N, hq, d), dtype=dtype, device=dev)
         os_ = hq * d
     else:
         _need_cuda("out", out, dev)
@@ -147,16 +142,11 @@ def prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k
     max_query_len, scale = int(max_query_len), float(scale)
     lib = library()
 
-    def call(ws, nbytes, stream):
-        return lib.pa_prefill_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                                  v_scale.data_ptr(), block_tables.data_ptr(), query_start.data_ptr(),
-                                  context_lens.data_ptr(), scale, out.data_ptr(), S, N, hq, hkv, d, bs, nb, ts,
-                                  max_query_len, qs, os_, _DTYPES[dtype], ws, nbytes, stream)
-
-    def size():
-        return int(lib.pa_prefill_fp8_workspace_size(S, N, hq, hkv, d, bs, max_query_len))
-
-    on_device(dev, _run, dev, "pa_prefill_fp8", size, call, workspace)
+    on_device(dev, _run, dev, "pa_prefill_fp8", lib.pa_prefill_fp8_workspace_size,
+              (S, N, hq, hkv, d, bs, max_query_len), lib.pa_prefill_fp8,
+              (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+               block_tables.data_ptr(), query_start.data_ptr(), context_lens.data_ptr(), scale, out.data_ptr(), S, N, hq,
+               hkv, d, bs, nb, ts, max_query_len, qs, os_, _DTYPES[dtype]), workspace)
     return out
 
 
