@@ -14,9 +14,8 @@
 //     weights stay in fp16's range whatever the scales are.  p is rounded to
 //     fp16 (half a step: 2^-11 of it; l adds the rounded values, a product of
 //     P with a row of ones, so weights still sum to one) -- the bytes carry
-//     2^-4.  Factor 2^7: weights down to
-//     2^-31 of the largest are kept, and the largest, 2^(7 + RESCALE_SLACK),
-//     fits.
+//     2^-4.  Factor 2^7: weights down to 2^-21 of the largest keep their bits,
+//     those down to 2^-31 some, and the largest, 2^(7 + RESCALE_SLACK), fits.
 // A query row in bf16 is scaled by a power of two to magnitudes in
 // [2^14, 2^15) and so becomes fp16 without loss (elements below 2^-28 of the
 // row's largest excepted); the power is undone with the score's scale.
