@@ -64,3 +64,21 @@ def test_rope_table_is_computed_in_64_bits():
         # float32 rounding of a value of size <= 1: half a step is 2^-25; the rest is float64's
         assert abs(t[p, i].item() - math.cos(a)) <= 2.0 ** -25 + 1e-10
         assert abs(t[p, 32 + i].item() - math.sin(a)) <= 2.0 ** -25 + 1e-10
+
+
+def test_binding_refuses_cpu_tensors_and_non_tensors():
+    import torch
+    f8 = torch.zeros((2, 1, 16, 64), dtype=torch.float8_e4m3fn)
+    h, s = torch.zeros((2, 1, 16, 64), dtype=torch.float16), torch.ones((2, 1))
+    x, i = torch.zeros((3, 1, 64), dtype=torch.float16), torch.zeros(3, dtype=torch.int64)
+    t, c = torch.zeros((3, 1), dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    cs = pa.rope_table(4, 64)
+    for call in (lambda: pa.rope_write_kv(x, x, x, h, h, i, i, cs), lambda: pa.write_kv_fp8(x, x, f8, f8, s, s, i),
+                 lambda: pa.rope_write_kv_fp8(x, x, x, f8, f8, s, s, i, i, cs),
+                 lambda: pa.decode_fp8(x, f8, f8, s, s, t, c, 0.1, 1),
+                 lambda: pa.prefill_fp8(x, f8, f8, s, s, t, torch.zeros(4, dtype=torch.int32), c, 0.1, 1),
+                 lambda: pa.copy_blocks_fp8(f8, f8, s, s, torch.zeros((1, 2), dtype=torch.int64)),
+                 lambda: pa.decode_fp8(x, None, f8, s, s, t, c, 0.1, 1),
+                 lambda: pa.write_kv_fp8(x, [1], f8, f8, s, s, i)):
+        with pytest.raises(pa.PagedAttentionError):
+            call()
