@@ -38,11 +38,10 @@
 #include "pa_kernels.cuh"
 #include "pa_mma.cuh"
 #include "pa_prefill.cuh"
+#include "pa_table_window.h"
 #include "pa_tcgen05.cuh"
 
 namespace pa {
-
-constexpr int TILE8 = 32;  // tokens per tile of the 8-bit kernels
 
 struct Decode8Args {
   // d.num_seqs counts row groups; d.q_seq_stride and d.out_seq_stride step from token to token; d.chunk_tiles counts
@@ -446,23 +445,19 @@ struct Math8 {
 // the row group's last tile are not read, and the one past its last block (an odd count of 16-token blocks) is never
 // used.
 struct TileLookup {
-  int win_s = -1, win_base = 0, ent = -1;
+  TableWindow win;
+  int ent = -1;
   // Tile j of row `s` (nt tiles): *p0 the block of its first 16 tokens, *p1 that of the other 16 (second: whether there
   // are such).  Returns whether the blocks lie in the pool.
   __device__ __forceinline__ bool find(const DecodeArgs &a, int s, int nt, int j, int L, int lane, int *p0, int *p1,
                                        bool *second) {
     const bool two = a.block_size == 16;
-    const int b0 = two ? 2 * j : j;
-    if (s != win_s || b0 < win_base || b0 >= win_base + 32) {
-      win_s = s;
-      win_base = b0 & ~31;
-      const int n = min(a.table_stride, two ? 2 * nt : nt);
-      ent = win_base + lane < n ? __ldg(a.block_tables + (long long)s * a.table_stride + win_base + lane) : -1;
-    }
+    if (win.ask(s, nt, j, L, a.block_size, a.table_stride))
+      ent = win.base + lane < win.end ? __ldg(a.block_tables + (long long)s * a.table_stride + win.base + lane) : -1;
     const unsigned nblocks = (unsigned)a.num_blocks;  // below 2^31, as are the rows (checked on the host)
-    *p0 = __shfl_sync(FULL, ent, b0 - win_base);
-    *p1 = two ? __shfl_sync(FULL, ent, (b0 + 1 - win_base) & 31) : *p0;  // b0 is even: the same window
-    *second = two && j * TILE8 + 16 < L;
+    *second = win.last > win.first;
+    *p0 = __shfl_sync(FULL, ent, win.first - win.base);
+    *p1 = two ? __shfl_sync(FULL, ent, (win.first + 1 - win.base) & 31) : *p0;
     return (unsigned)*p0 < nblocks && (!*second || (unsigned)*p1 < nblocks);
   }
 };

@@ -1,0 +1,36 @@
+// Which entries of a block table row a warp of the 8-bit decode kernels holds: one per lane, of the row it read last.
+// Host code too, so that the choice can be tested without a GPU.
+#pragma once
+
+#ifdef __CUDACC__
+#define PA_HOST_DEVICE __host__ __device__ __forceinline__
+#else
+#define PA_HOST_DEVICE inline
+#endif
+
+namespace pa {
+
+constexpr int TILE8 = 32;  // tokens per tile of the 8-bit kernels
+
+struct TableWindow {
+  int row = -1, base = 0, end = 0;  // lane i holds entry base + i of table row `row` while that is below `end`
+  int first = 0, last = 0;          // entries of the tile asked for last
+
+  // Asks for the entries of tile j of a row group that sees L > 0 tokens, in nt tiles, of table row r.  Returns whether
+  // the lanes have to be loaded, with entries base .. end - 1.  Row groups of one sequence share its row, and a later
+  // one may need an entry that an earlier one did not load: holding the row and the window is not enough.
+  PA_HOST_DEVICE bool ask(int r, int nt, int j, int L, int block_size, int table_stride) {
+    const bool two = block_size == 16;
+    first = two ? 2 * j : j;
+    last = two && j * TILE8 + 16 < L ? first + 1 : first;  // first is even: the same window
+    if (r == row && first >= base && last < end) return false;
+    const int n = two ? 2 * nt : nt;
+    row = r;
+    base = first & ~31;
+    end = base + 32 < n ? base + 32 : n;
+    if (end > table_stride) end = table_stride;
+    return true;
+  }
+};
+
+}  // namespace pa
