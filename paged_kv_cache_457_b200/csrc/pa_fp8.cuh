@@ -442,18 +442,21 @@ struct Math8 {
 };
 
 // The physical blocks of a unit's tiles, through a 32-entry window of the table row (one entry per lane).  Entries past
-// the row group's last tile are not read, and the one past its last block (an odd count of 16-token blocks) is never
-// used.
+// the row group's last block are not read.
 struct TileLookup {
   TableWindow win;
   int ent = -1;
-  // Tile j of row `s` (nt tiles): *p0 the block of its first 16 tokens, *p1 that of the other 16 (second: whether there
-  // are such).  Returns whether the blocks lie in the pool.
-  __device__ __forceinline__ bool find(const DecodeArgs &a, int s, int nt, int j, int L, int lane, int *p0, int *p1,
+  // Tile j of row `s`, of a group that sees L tokens: *p0 the block of its first 16 tokens, *p1 that of the other 16
+  // (second: whether there are such).  Returns whether the blocks lie in the pool.
+  __device__ __forceinline__ bool find(const DecodeArgs &a, int s, int j, int L, int lane, int *p0, int *p1,
                                        bool *second) {
     const bool two = a.block_size == 16;
-    if (win.ask(s, nt, j, L, a.block_size, a.table_stride))
-      ent = win.base + lane < win.end ? __ldg(a.block_tables + (long long)s * a.table_stride + win.base + lane) : -1;
+    if (win.ask(s, j, L, a.block_size)) {
+      const int e = win.base + lane;
+      ent = e < win.end && dcheck((long long)e * a.block_size < L && e < a.table_stride)
+                ? __ldg(a.block_tables + (long long)s * a.table_stride + e)
+                : -1;
+    }
     const unsigned nblocks = (unsigned)a.num_blocks;  // below 2^31, as are the rows (checked on the host)
     *second = win.last > win.first;
     *p0 = __shfl_sync(FULL, ent, win.first - win.base);
@@ -558,7 +561,7 @@ __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     }
     int p0, p1;
     bool second;
-    const bool found = look.find(a, prod_row, pos.nt, pos.j, prod_L, lane, &p0, &p1, &second);
+    const bool found = look.find(a, prod_row, pos.j, prod_L, lane, &p0, &p1, &second);
     const bool good = found && dcheck(h < a.num_kv_heads && pos.j * TILE8 < prod_L);
     const bool whole = second || a.block_size != 16;  // both halves are copied
     bad_slots = good ? (bad_slots & ~(1u << st)) : (bad_slots | (1u << st));
@@ -865,7 +868,7 @@ __global__ void __launch_bounds__(WARPS * 32, 3) decode8_segment_kernel(const De
     const int j = warp + t * WARPS;
     int p0, p1;
     bool second;
-    const bool good = look.find(a, g.s, nt, j, g.L, lane, &p0, &p1, &second) && dcheck(h < a.num_kv_heads);
+    const bool good = look.find(a, g.s, j, g.L, lane, &p0, &p1, &second) && dcheck(h < a.num_kv_heads);
     bad |= !good;
     unsigned char *kd = ring + (t % Smem::STAGES) * Smem::STAGE_BYTES;
     if (good) {

@@ -16,19 +16,19 @@ struct TableWindow {
   int row = -1, base = 0, end = 0;  // lane i holds entry base + i of table row `row` while that is below `end`
   int first = 0, last = 0;          // entries of the tile asked for last
 
-  // Asks for the entries of tile j of a row group that sees L > 0 tokens, in nt tiles, of table row r.  Returns whether
-  // the lanes have to be loaded, with entries base .. end - 1.  Row groups of one sequence share its row, and a later
-  // one may need an entry that an earlier one did not load: holding the row and the window is not enough.
-  PA_HOST_DEVICE bool ask(int r, int nt, int j, int L, int block_size, int table_stride) {
+  // Asks for the entries (of blocks of 16 or 32 tokens) of tile j of a row group that sees L > 0 tokens of table row r.
+  // Returns whether the lanes have to be loaded, with entries base .. end - 1: none behind the group's last block, since
+  // the row may be the last of a table that ends there.  Row groups of one sequence share its row, and a later one may
+  // need an entry that an earlier one did not load: holding the row and the window is not enough.
+  PA_HOST_DEVICE bool ask(int r, int j, int L, int block_size) {
     const bool two = block_size == 16;
     first = two ? 2 * j : j;
-    last = two && j * TILE8 + 16 < L ? first + 1 : first;  // first is even: the same window
+    last = two && L - j * TILE8 > 16 ? first + 1 : first;  // first is even: the same window
     if (r == row && first >= base && last < end) return false;
-    const int n = two ? 2 * nt : nt;
+    const int blocks = ((L - 1) >> (two ? 4 : 5)) + 1;  // at most the row's entries: contexts are checked against them
     row = r;
     base = first & ~31;
-    end = base + 32 < n ? base + 32 : n;
-    if (end > table_stride) end = table_stride;
+    end = base + 32 < blocks ? base + 32 : blocks;
     return true;
   }
 };

@@ -39,7 +39,7 @@ int main(int argc, char **argv) {
       std::vector<int> held(32, -1);  // the row * stride + entry that each lane holds
       for (size_t t = at; t < stream.size() && t < at + (size_t)chunk; ++t) {
         const Group &g = groups[stream[t].g];
-        if (w.ask(g.s, g.nt, stream[t].j, g.L, bs, stride)) {
+        if (w.ask(g.s, stream[t].j, g.L, bs)) {
           ++loads;
           for (int i = 0; i < 32; ++i) held[i] = w.base + i < w.end ? g.s * stride + w.base + i : -1;
           if (w.end > (g.L + bs - 1) / bs) ++past;  // an entry behind the last one that the group needs

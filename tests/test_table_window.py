@@ -28,3 +28,12 @@ def test_every_entry_a_tile_needs_is_held(walk, bs, new, per, longest):
     for seed in range(4):
         missing, _, loads = walk(seed, bs, new, per, longest)
         assert missing == 0 and loads > 0
+
+
+@pytest.mark.parametrize("bs", [16, 32])
+@pytest.mark.parametrize("new,per,longest", [(9, 2, 500), (24, 8, 200), (1, 1, 3000), (1, 1, 15)])
+def test_no_entry_behind_a_groups_last_block_is_read(walk, bs, new, per, longest):
+    """The row may be the last of a table that ends with that entry."""
+    for seed in range(4):
+        _, past, loads = walk(seed, bs, new, per, longest)
+        assert past == 0 and loads > 0
