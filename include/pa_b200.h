@@ -512,7 +512,9 @@ int pa_decode_cascade(const void *q, const void *k_cache, const void *v_cache, c
  * block_size must not exceed 2^31 - 1 (PA_ERR_SHAPE).  Caches are 16-byte
  * aligned, scales 4-byte.
  * The workspace (pa_decode_fp8_workspace_size bytes, 16-byte aligned; small
- * calls need none) is scratch of one call in flight at a time.
+ * calls need none) is scratch of one call in flight at a time.  A call
+ * enqueues more than one operation on it: host threads that share one issue
+ * their calls one after another, on the same stream too.
  */
 size_t pa_decode_fp8_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                     int32_t block_size, int32_t max_context_len, int32_t partition_tokens);
@@ -538,7 +540,8 @@ int pa_decode_fp8(const void *q, const void *k_cache, const void *v_cache, const
  * of its rows in the call.
  *   workspace   device scratch of pa_prefill_fp8_workspace_size bytes,
  *               16-byte aligned; needs no initialisation.  Calls that may run
- *               at the same time must not share one.
+ *               at the same time must not share one; host threads as for
+ *               pa_decode_fp8.
  */
 size_t pa_prefill_fp8_workspace_size(int32_t num_seqs, int64_t num_query_tokens, int32_t num_q_heads,
                                      int32_t num_kv_heads, int32_t head_dim, int32_t block_size,

@@ -196,6 +196,9 @@ def write_kv(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: t
 
 
 _workspaces: dict = {}
+# Held while a call enqueues its operations on a kept workspace: host threads on one stream share that workspace, and the
+# operations of two calls must not mix (the library call runs without the interpreter's lock).
+_workspace_use = threading.RLock()
 
 
 def decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
@@ -213,6 +216,15 @@ def _workspace(dev: torch.device, stream: int, nbytes: int) -> torch.Tensor | No
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         _workspaces[key] = ws
     return ws
+
+
+def _enqueue(call, args, workspace: torch.Tensor | None, dev: torch.device, stream: int, need: int) -> int:
+    """call(*args, workspace pointer, bytes, stream) with the caller's workspace, or the kept one of `need` bytes."""
+    if workspace is not None:
+        return call(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
+    with _workspace_use:
+        ws = _workspace(dev, stream, need)
+        return call(*args, ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, stream)
 
 
 def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -248,14 +260,11 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     stream = _stream(dev)
     lib = load_library()
     need = int(lib.pa_decode_workspace_size(S, hq, hkv, d, bs, int(max_context_len), int(partition_tokens)))
-    if workspace is None:
-        workspace = _workspace(dev, stream, need)
-    rc = lib.pa_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-                       context_lens.data_ptr(), float(scale), out.data_ptr(), S, hq, hkv, d, bs, nb,
-                       int(block_tables.stride(0)) if S else 1, int(max_context_len), q.stride(0) if S else hq * d,
-                       out.stride(0) if S else hq * d, int(partition_tokens), _DTYPES[q.dtype],
-                       workspace.data_ptr() if workspace is not None else None,
-                       workspace.numel() * workspace.element_size() if workspace is not None else 0, stream)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+            float(scale), out.data_ptr(), S, hq, hkv, d, bs, nb, int(block_tables.stride(0)) if S else 1,
+            int(max_context_len), q.stride(0) if S else hq * d, out.stride(0) if S else hq * d, int(partition_tokens),
+            _DTYPES[q.dtype])
+    rc = _enqueue(lib.pa_decode, args, workspace, dev, stream, need)
     _check(rc, "pa_decode")
     return out
 

@@ -114,7 +114,7 @@ def decode_cascade(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                    context_lens: torch.Tensor, scale: float, plan: CascadePlan, plan_device: torch.Tensor,
                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """:func:`decode` through a cascade plan; ``plan_device`` is ``plan.plan`` in device memory."""
-    from . import (PagedAttentionError, _DTYPES, _cache_geometry, _check, _need_cuda, _stream, _workspace,
+    from . import (PagedAttentionError, _DTYPES, _cache_geometry, _check, _enqueue, _need_cuda, _stream,
                    load_library)
     dev = k_cache.device
     for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
@@ -143,13 +143,10 @@ def decode_cascade(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
             raise PagedAttentionError("out must be [S, Hq, d] with q's dtype, heads and dims contiguous")
     lib = load_library()
     stream = _stream(dev)
-    if workspace is None:
-        workspace = _workspace(dev, stream, int(lib.pa_cascade_workspace_size(ctypes.byref(info), d)))
-    rc = lib.pa_decode_cascade(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-                               context_lens.data_ptr(), float(scale), out.data_ptr(), d, nb,
-                               int(block_tables.stride(0)) if S else 1, q.stride(0) if S else hq * d,
-                               out.stride(0) if S else hq * d, _DTYPES[q.dtype], plan_device.data_ptr(),
-                               ctypes.byref(info), workspace.data_ptr() if workspace is not None else None,
-                               workspace.numel() * workspace.element_size() if workspace is not None else 0, stream)
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+            float(scale), out.data_ptr(), d, nb, int(block_tables.stride(0)) if S else 1, q.stride(0) if S else hq * d,
+            out.stride(0) if S else hq * d, _DTYPES[q.dtype], plan_device.data_ptr(), ctypes.byref(info))
+    rc = _enqueue(lib.pa_decode_cascade, args, workspace, dev, stream,
+                  int(lib.pa_cascade_workspace_size(ctypes.byref(info), d)))
     _check(rc, "pa_decode_cascade")
     return out

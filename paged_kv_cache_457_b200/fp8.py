@@ -8,7 +8,7 @@ import ctypes
 
 import torch
 
-from . import PagedAttentionError, _DTYPES, _check, _mapping, _need_cuda, _workspace, _workspaces
+from . import PagedAttentionError, _DTYPES, _check, _mapping, _need_cuda, _workspace, _workspace_use, _workspaces
 from .append import fp8_geometry, library, need_cuda, on_device, same_device, stream_of, token_stride
 
 PA_ERR_WORKSPACE = -7
@@ -49,8 +49,8 @@ def _tables(block_tables: torch.Tensor, context_lens: torch.Tensor, S: int) -> i
 
 def _run(dev, what, size, sizes, call, args, workspace):
     """call(*args, workspace pointer, bytes, stream) with the caller's workspace, or with one kept per device and stream
-    (of size(*sizes) bytes).  A capture gets its own, from the graph's pool: a captured graph may be replayed beside
-    other calls and must neither share theirs nor outlive it."""
+    (of size(*sizes) bytes), on which one call at a time enqueues its operations.  A capture gets its own, from the
+    graph's pool: a captured graph may be replayed beside other calls and must neither share theirs nor outlive it."""
     stream = stream_of(dev)
     if workspace is not None:
         if workspace.device != dev or not workspace.is_contiguous():
@@ -61,11 +61,12 @@ def _run(dev, what, size, sizes, call, args, workspace):
         ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
         rc = call(*args, ws.data_ptr() if n else None, n, stream)
     else:
-        ws = _workspaces.get((dev.index, stream))
-        rc = call(*args, ws.data_ptr(), ws.numel(), stream) if ws is not None else call(*args, None, 0, stream)
-        if rc == PA_ERR_WORKSPACE:
-            ws = _workspace(dev, stream, int(size(*sizes)))
-            rc = call(*args, ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, stream)
+        with _workspace_use:
+            ws = _workspaces.get((dev.index, stream))
+            rc = call(*args, ws.data_ptr(), ws.numel(), stream) if ws is not None else call(*args, None, 0, stream)
+            if rc == PA_ERR_WORKSPACE:
+                ws = _workspace(dev, stream, int(size(*sizes)))
+                rc = call(*args, ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, stream)
     if rc:
         _check(rc, what)
 
