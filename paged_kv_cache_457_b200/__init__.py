@@ -207,14 +207,15 @@ def decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_s
                                                        max_context_len, partition_tokens))
 
 
-def _workspace(dev: torch.device, stream: int, nbytes: int) -> torch.Tensor | None:
+def _workspace(dev: torch.device, stream: int, nbytes: int, kept: dict | None = None) -> torch.Tensor | None:
     if nbytes == 0:
         return None
+    kept = _workspaces if kept is None else kept
     key = (dev.index, stream)
-    ws = _workspaces.get(key)
+    ws = kept.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _workspaces[key] = ws
+        kept[key] = ws
     return ws
 
 

@@ -8,10 +8,14 @@ import ctypes
 
 import torch
 
-from . import PagedAttentionError, _DTYPES, _check, _mapping, _need_cuda, _workspace, _workspace_use, _workspaces
+from . import PagedAttentionError, _DTYPES, _check, _mapping, _need_cuda, _workspace, _workspace_use
 from .append import fp8_geometry, library, need_cuda, on_device, same_device, stream_of, token_stride
 
 PA_ERR_WORKSPACE = -7
+
+# Kept apart from the 16-bit calls' workspaces: a captured graph of those goes on using the one kept for its stream, which a
+# call here that needs more would free.
+_workspaces: dict = {}
 
 
 def bind(lib: ctypes.CDLL) -> None:
@@ -65,7 +69,7 @@ def _run(dev, what, size, sizes, call, args, workspace):
             ws = _workspaces.get((dev.index, stream))
             rc = call(*args, ws.data_ptr(), ws.numel(), stream) if ws is not None else call(*args, None, 0, stream)
             if rc == PA_ERR_WORKSPACE:
-                ws = _workspace(dev, stream, int(size(*sizes)))
+                ws = _workspace(dev, stream, int(size(*sizes)), _workspaces)
                 rc = call(*args, ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, stream)
     if rc:
         _check(rc, what)

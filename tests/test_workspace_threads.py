@@ -44,7 +44,7 @@ def lib(monkeypatch):
     monkeypatch.setattr(fp8, "stream_of", lambda dev: 7)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(pa, "_workspaces", {})
-    monkeypatch.setattr(fp8, "_workspaces", pa._workspaces)
+    monkeypatch.setattr(fp8, "_workspaces", {})
     lib.plan = plan
     return lib
 
@@ -95,3 +95,23 @@ def test_a_workspace_of_the_callers_own_is_not_waited_for(lib):
     for t in threads:
         t.join()
     assert lib.most == 2
+
+
+def test_8_bit_calls_leave_the_16_bit_calls_workspace_alone(lib, monkeypatch):
+    """A captured decode graph goes on using the workspace that was kept for its stream: an 8-bit call there that needs
+    a larger one neither frees it nor works in it."""
+    q = torch.zeros((2, 4, 64), dtype=torch.float16)
+    cache = torch.zeros((8, 2, 16, 64), dtype=torch.float16)
+    tables, ctx = torch.zeros((2, 4), dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    pa.decode(q, cache, cache, tables, ctx, 0.1, 32)
+    ours = pa._workspaces[(None, 7)]
+    used = []
+
+    def call(*args):
+        used.append(args[-3])
+        return 0 if args[-2] >= 4096 else fp8.PA_ERR_WORKSPACE
+    fp8._run(torch.device("cpu"), "pa_decode_fp8", lambda: 4096, (), call, (), None)
+    assert pa._workspaces[(None, 7)] is ours
+    assert ours.data_ptr() not in used
+    pa.decode(q, cache, cache, tables, ctx, 0.1, 32)
+    assert lib.calls[-1][1][-3] == ours.data_ptr()
