@@ -319,8 +319,18 @@ struct Math8 {
       }
       clear_tail(vt, nvalid, lane);
     }
-    // a scale of zero (a block of zeros) would send the exponent to -inf: its bytes are zeros, any small scale will do
-    const float lv[2] = {lg2(fmaxf(sc4.z, 5.421011e-20f)), lg2(fmaxf(sc4.w, 5.421011e-20f))};
+    // log2 of V's scales; one below 2^-80 counts as zero (l, in units of 1 / scale, then fits fp32 whatever the length).
+    // Under such a scale no weight multiplies the bytes, but all count in l: any exponent would do for them, and the
+    // largest scale's so far keeps them near the others
+    float lr[2] = {lg2(sc4.z), lg2(sc4.w)};
+    lv_top = fmax3(lv_top, lr[0], lr[1]);
+    const float low = fmaxf(lv_top, -80.f);
+    float lv[2];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      if (lr[mt] < -80.f) lr[mt] = -INFINITY;
+      lv[mt] = lr[mt] == -INFINITY ? low : lr[mt];
+    }
     const float ka[2] = {sc4.x * qa, sc4.y * qa}, kb[2] = {sc4.x * qbs, sc4.y * qbs};
     // exponents of the weights, e = z + lv - (m - 7); dead rows -inf
     float e[2][4];
@@ -369,11 +379,12 @@ struct Math8 {
         o[c][2] *= fa;
         o[c][3] *= fb;
       }
-      la *= fa;
-      lb *= fb;
+      // l in two steps: it is in units of 1 / scale, and m moves by the quotient of two scales
+      const float ha = ma > -INFINITY ? ex2(0.5f * (oa - ma)) : 0.f, hb = mb > -INFINITY ? ex2(0.5f * (ob - mb)) : 0.f;
+      la = la * ha * ha;
+      lb = lb * hb * hb;
       exponents();
     }
-    lv_top = fmax3(lv_top, lv[0], lv[1]);
     uint32_t pb[2][2];
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
@@ -384,17 +395,19 @@ struct Math8 {
       float ls[4] = {0.f, 0.f, 0.f, 0.f};
       const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
       mma_16816_f16(ls, ones, pb[mt][0], pb[mt][1]);
-      float sa = ls[0], sb = ls[1];
-      if (lv[mt] < lv_top - 10.f) {  // uniform, rare: under a scale this small fp16 has lost weights that count in l
-        sa = p0 + p2;
-        sb = p1 + p3;
+      float sa = ls[0], sb = ls[1], iv = ex2(-lv[mt]);
+      if (lr[mt] < low - 10.f) {  // uniform, rare: under a scale this small fp16 has lost weights that count in l
+        const float up = fminf(low - lv[mt], 112.f);  // and fp32 too when it is very small
+        sa = ex2(e[mt][0] + up) + ex2(e[mt][2] + up);
+        sb = ex2(e[mt][1] + up) + ex2(e[mt][3] + up);
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
           sa += __shfl_xor_sync(FULL, sa, off);
           sb += __shfl_xor_sync(FULL, sb, off);
         }
+        iv = ex2(-lv[mt] - up);
+        if (lr[mt] == -INFINITY) pb[mt][0] = pb[mt][1] = 0;
       }
-      const float iv = ex2(-lv[mt]);
       la = fmaf(sa, iv, la);
       lb = fmaf(sb, iv, lb);
     }
@@ -464,6 +477,13 @@ struct TileLookup {
     return (unsigned)*p0 < nblocks && (!*second || (unsigned)*p1 < nblocks);
   }
 };
+
+// A piece's normaliser l (in units of 1 / scale) from its own exponent m to M, in two steps: 2^(m - M), with the quotient
+// of two scales in it, may leave fp32's range where the product does not.
+__device__ __forceinline__ float weighted_sum(float2 ml, float M) {
+  const float h = exp2f(0.5f * (ml.x - M));
+  return ml.y * h * h;
+}
 
 // Decode split kernel: the work decomposition of decode_split_mma_kernel (a balanced stream of tiles cut into chunks,
 // pieces merged by a second kernel) on tiles of 32 tokens and units of a row group and a head chunk; K and V tiles
@@ -766,7 +786,7 @@ __global__ void __launch_bounds__(256, 1) decode8_merge_kernel(const Decode8Args
 #pragma unroll
       for (int x = 0; x < HW; ++x) {
         wt[x] = lane < n ? exp2f(ml0[x].x - M[x]) : 0.f;
-        l[x] = ml0[x].y * wt[x];
+        l[x] = lane < n ? weighted_sum(ml0[x], M[x]) : 0.f;
       }
       for (int base = 0; base < n; base += MB) {
         if (base > 0) {
@@ -777,7 +797,7 @@ __global__ void __launch_bounds__(256, 1) decode8_merge_kernel(const Decode8Args
             for (int x = 0; x < HW; ++x) {
               const float2 ml = p < n ? __ldg(a.ws_ml + r + x) : make_float2(-INFINITY, 0.f);
               wt[x] = p < n ? exp2f(ml.x - M[x]) : 0.f;
-              l[x] = fmaf(ml.y, wt[x], l[x]);
+              if (p < n) l[x] += weighted_sum(ml, M[x]);
             }
           }
           load_batch(base);
@@ -942,7 +962,7 @@ __global__ void __launch_bounds__(WARPS * 32, 3) decode8_segment_kernel(const De
     for (int w = 0; w < WARPS; ++w) {
       const float2 ml = x_ml[w * 8 + c];
       const float wt = ml.y != 0.f ? exp2f(ml.x - M) : 0.f;  // a warp without keys for this column: m = -inf, l = 0
-      l = fmaf(ml.y, wt, l);
+      if (ml.y != 0.f) l += weighted_sum(ml, M);
       const float *src = x_acc + (w * 8 + c) * D + d0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = fmaf(wt, src[e], f[e]);
