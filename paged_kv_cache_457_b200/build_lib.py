@@ -36,9 +36,8 @@ def nvcc() -> str:
 def command(out: str = LIB, verbose_ptxas: bool = False, debug: bool = False) -> list:
     cmd = [nvcc(), "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
            "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-o", out] + SOURCES
-    if debug:
-        # optimised on all cores, which the release build is not: it changes the kernels' code
-        cmd[1:1] = ["-DPA_DEBUG", "--split-compile=0"]
+    if debug:  # the release build's options otherwise: others would change the code that the checks are to speak for
+        cmd[1:1] = ["-DPA_DEBUG"]
     if verbose_ptxas:
         cmd[1:1] = ["-Xptxas", "-v"]
     return cmd
