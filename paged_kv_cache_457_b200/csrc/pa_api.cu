@@ -669,8 +669,8 @@ int append_fp8(pa::AppendArgs &a, int head_dim, int dtype, bool rope, bool inter
 
 // ---- decode over 8-bit caches (pa_fp8.cuh)
 
-// Launch shape of the 8-bit split kernel: 12 warps of two 8 KB slots on an SM.  Measured on 64 sequences of 32 heads: 109
-// us; 8 warps of three slots 125, 16 warps of two (128 registers) 120.
+// Launch shape of the 8-bit split kernel: 12 warps of two 8 KB slots on an SM.  Measured on 64 sequences of 32 heads 89
+// us, on 256 of 32 q / 8 kv heads 107, on 8 long contexts 268; 8 warps of three slots 105, 123 and 279.
 constexpr int kWarps8 = 4, kStages8 = 2, kBlocks8 = 3;
 static_assert(kWarps8 == kWarps, "blocks_per_sm sizes blocks with kWarps warps");
 
@@ -840,9 +840,10 @@ int run_decode8(pa::Decode8Args &args, const LaunchPlan &lp, int head_dim, int d
 
 // A prefill call of few tokens per sequence runs on the decode kernels, a row group per tokens that fill the eight
 // columns; more go to the 128-row tiles of prefill8_tc_kernel, whose time hardly depends on the tokens while a tile holds
-// them.  Measured, this against those: 64 sequences of up to 2000 tokens, 32 q / 8 kv heads, 8 / 16 / 24 / 32 tokens each
-// 126 / 229 / 330 / 434 against 376 / 379 / 380 / 383 us, with 32 kv heads 132 / 231 / 332 / 438 against 375 to 382; 4 of
-// up to 16000 tokens 71 / 132 / 181 / 230 against 256.  Many row groups keep to those tiles too: every block of the split
+// them.  Measured, this against those: 64 sequences of up to 2000 tokens, 32 q / 8 kv heads, 8 / 16 / 24 tokens each
+// 126 / 230 / 340 against 358 / 359 / 363 us, with 32 kv heads 132 / 232 / 332 against 357 / 359 / 362; 4 of up to 16000
+// tokens 52 / 89 / 128 against 215.  (The time grows by about 100 us for 8 tokens more: at 32 the tiles are ahead.)  Many
+// row groups keep to those tiles too: every block of the split
 // kernel walks all of their lengths.
 constexpr int kFewTokens8 = 24, kFewGroups8 = 4096;
 struct FewTokens {

@@ -14,7 +14,9 @@
 //     weights stay in fp16's range whatever the scales are.  p is rounded to
 //     fp16 (half a step: 2^-11 of it; l adds the rounded values, a product of
 //     P with a row of ones, so weights still sum to one) -- the bytes carry
-//     2^-4.  Factor 2^7: weights down to 2^-21 of the largest keep their bits,
+//     2^-4.  The 16-bit kernels multiply the rounding's residual as well, which
+//     here would double the products of V for an error of fp16 outputs of
+//     0.00021 instead of 0.00025, bf16 outputs the same.  Factor 2^7: weights down to 2^-21 of the largest keep their bits,
 //     those down to 2^-31 some, and the largest, 2^(7 + RESCALE_SLACK), fits.
 // A query row in bf16 is scaled by a power of two to magnitudes in
 // [2^14, 2^15) and so becomes fp16 without loss (elements below 2^-28 of the
@@ -107,9 +109,9 @@ __device__ __forceinline__ int group_tiles(const RowGroup &g) {
 }
 
 // The cut of the tile stream (see ChunkPlan): uniform chunks, `tail` of them per warp on average.  Long streams take
-// several, so that warps that run ahead take over from those that lag (8 contexts of 16k-32k tokens: 278, 268, 265 and
-// 264 us with 1, 2, 3 and 5); short ones one, since each cut leaves pieces to merge (256 sequences of 32 q / 8 kv
-// heads, 31 tiles per warp: 104, 105, 107 and 109 us).
+// several, so that warps that run ahead take over from those that lag (8 contexts of 16k-32k tokens: 278 us with one,
+// 268 with three); short ones one, since each cut leaves pieces to merge (256 sequences of 32 q / 8 kv heads, 31 tiles
+// per warp: 1, 3 and 5 us more with two, three and five).
 constexpr int TAIL8_TILES = 16, TAIL8_MOST = 3, MIN_CHUNK8_TILES = 2;
 __device__ __forceinline__ ChunkPlan plan_chunks8(const DecodeArgs &a, int tiles_per_head_chunk_set) {
   ChunkPlan p;
@@ -489,8 +491,8 @@ __device__ __forceinline__ float weighted_sum(float2 ml, float M) {
 // pieces merged by a second kernel) on tiles of 32 tokens and units of a row group and a head chunk; K and V tiles
 // arrive by TMA, the tile's scales by 4-byte asynchronous copies that complete on the same barrier.
 // Bound by HBM on long streams: 8 contexts of 16k-32k tokens (1.68 GB) take 268 us, 0.95 of the measured copy rate; 64
-// sequences of 32 heads (476 MB) 89 us, 0.81; 256 of 32 q / 8 kv heads with a long tail of lengths (484 MB) 105 us,
-// 0.70: there every warp meets two or three pieces (query rows, partial states) per 31 tiles, and the stream's end is
+// sequences of 32 heads (476 MB) 89 us, 0.81; 256 of 32 q / 8 kv heads with a long tail of lengths (484 MB) 107 us,
+// 0.69: there every warp meets two or three pieces (query rows, partial states) per 31 tiles, and the stream's end is
 // uneven.  A tile costs a warp about 2 us at 12 warps on an SM; widening the bytes (128 cvt per tile) and the products
 // share the issue slots about evenly.
 template <class E, int D, int WARPS, int STAGES, int BLOCKS, bool FEW>
