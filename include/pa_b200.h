@@ -508,7 +508,7 @@ int pa_decode_cascade(const void *q, const void *k_cache, const void *v_cache, c
  * rounded; products below 2^-21 of the largest so far keep fewer bits (to
  * 2^-31), which only V scales that far apart in one context could show.  A
  * V scale below 2^-80 counts as zero.  partition_tokens counts tokens per
- * chunk, rounded up to 32.  K/V bytes of rows past a context, and entries
+ * chunk, rounded up to a multiple of 32, and to 64 at least.  K/V bytes of rows past a context, and entries
  * past its last block, may hold anything.  num_blocks * num_kv_heads *
  * block_size must not exceed 2^31 - 1 (PA_ERR_SHAPE).  Caches are 16-byte
  * aligned, scales 4-byte.

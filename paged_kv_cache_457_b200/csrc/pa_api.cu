@@ -671,7 +671,7 @@ int append_fp8(pa::AppendArgs &a, int head_dim, int dtype, bool rope, bool inter
 
 // Launch shape of the 8-bit split kernel: 12 warps of two 8 KB slots on an SM.  Measured on 64 sequences of 32 heads 89
 // us, on 256 of 32 q / 8 kv heads 107, on 8 long contexts 268; 8 warps of three slots 105, 123 and 279.
-constexpr int kWarps8 = 4, kStages8 = 2, kBlocks8 = 3;
+constexpr int kWarps8 = 4, kStages8 = pa::STAGES8, kBlocks8 = 3;
 static_assert(kWarps8 == kWarps, "blocks_per_sm sizes blocks with kWarps warps");
 
 // Query heads handled together: the largest divisor of the group not above 8 (the mma's columns); one kernel serves

@@ -37,6 +37,7 @@
 #include <cuda.h>
 
 #include "pa_append.cuh"
+#include "pa_chunk8.h"
 #include "pa_kernels.cuh"
 #include "pa_mma.cuh"
 #include "pa_prefill.cuh"
@@ -108,28 +109,13 @@ __device__ __forceinline__ int group_tiles(const RowGroup &g) {
   return g.cnt > 0 && g.L > 0 ? (g.L + TILE8 - 1) / TILE8 : 0;
 }
 
-// The cut of the tile stream (see ChunkPlan): uniform chunks, `tail` of them per warp on average.  Long streams take
-// several, so that warps that run ahead take over from those that lag (8 contexts of 16k-32k tokens: 278 us with one,
-// 268 with three); short ones one, since each cut leaves pieces to merge (256 sequences of 32 q / 8 kv heads, 31 tiles
-// per warp: 1, 3 and 5 us more with two, three and five).
-constexpr int TAIL8_TILES = 16, TAIL8_MOST = 3, MIN_CHUNK8_TILES = 2;
+// The cut of the tile stream (see ChunkPlan).
 __device__ __forceinline__ ChunkPlan plan_chunks8(const DecodeArgs &a, int tiles_per_head_chunk_set) {
   ChunkPlan p;
   p.total = (long long)tiles_per_head_chunk_set * a.num_kv_heads * a.n_chunks;
-  const long long W = a.split_warps;
-  auto ceil_div = [](long long x, long long y) {
-    return x < 0x7fffffffLL && y < 0x7fffffffLL ? (long long)(((unsigned)x + (unsigned)y - 1u) / (unsigned)y)
-                                                 : (x + y - 1) / y;
-  };
-  long long c = a.chunk_tiles;
-  if (c == 0) {
-    const long long tail = max(1LL, min((long long)TAIL8_MOST, p.total / (W * TAIL8_TILES)));
-    c = max((long long)MIN_CHUNK8_TILES, ceil_div(p.total, W * tail));
-  }
-  c = max(c, ceil_div(p.total, a.max_chunks));  // never more chunks than the workspace holds
-  p.c1 = p.c2 = max(c, 1LL);
-  p.count = ceil_div(p.total, p.c1);
-  p.n1 = min(W, p.count);
+  p.c1 = p.c2 = chunk8_tiles(p.total, a.split_warps, a.chunk_tiles, a.max_chunks);
+  p.count = ceil_div8(p.total, p.c1);
+  p.n1 = min((long long)a.split_warps, p.count);
   return p;
 }
 
@@ -499,6 +485,7 @@ template <class E, int D, int WARPS, int STAGES, int BLOCKS, bool FEW>
 __global__ void __launch_bounds__(WARPS * 32, BLOCKS)
     decode8_split_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                          const Decode8Args args) {
+  static_assert(STAGES <= MIN_CHUNK8_TILES, "see there");
   const DecodeArgs &a = args.d;
   using Smem = Smem8<D, WARPS, STAGES>;
   constexpr int KSTEPS = D / 16;

@@ -2,10 +2,12 @@
 // Host code too, so that the choice can be tested without a GPU.
 #pragma once
 
+#ifndef PA_HOST_DEVICE
 #ifdef __CUDACC__
 #define PA_HOST_DEVICE __host__ __device__ __forceinline__
 #else
 #define PA_HOST_DEVICE inline
+#endif
 #endif
 
 namespace pa {

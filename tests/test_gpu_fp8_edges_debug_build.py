@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CASES = ["tests/test_gpu_fp8_row_groups.py", "tests/test_gpu_fp8_table_views.py", "tests/test_gpu_fp8_v_scales.py",
-         "tests/test_gpu_fp8_hints.py", "tests/test_gpu_append_long.py::test_head_counts_that_do_not_divide",
+         "tests/test_gpu_fp8_hints.py", "tests/test_gpu_fp8_small_chunks.py", "tests/test_gpu_append_long.py::test_head_counts_that_do_not_divide",
          "tests/test_gpu_append_long.py::test_queries_turned_in_place"]
 
 
