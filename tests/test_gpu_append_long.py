@@ -12,7 +12,7 @@ import torch
 import fp8_ref as R
 import paged_kv_cache_457_b200 as pa
 from gpu_util import TORCH_DT, require_gpu
-from test_gpu_append import check_fp8, dev, f8, fp8_state, round_to, rows, token_mix
+from test_gpu_append import check_fp8, dev, f8, round_to, rows, token_mix
 
 pytestmark = pytest.mark.gpu
 
@@ -45,6 +45,16 @@ def prompts(rng, bs, T):
     return nb + 8, np.array(out_s, np.int64), np.array(out_p, np.int64)
 
 
+def random_state(rng, nb, hkv, bs, d):
+    """Bytes of any finite value with power-of-two scales around those of the rows."""
+    out = []
+    for _ in range(2):
+        b = rng.integers(0, 256, (nb, hkv, bs, d), dtype=np.uint8)
+        b[(b & 0x7F) == 0x7F] = 0
+        out += [b, np.exp2(rng.integers(-10, -4, (nb, hkv))).astype(np.float32)]
+    return out
+
+
 def run(rng, dtype, hq, hkv, d, bs, rot, il, T, want_heads, rope=True, in_place=False, some=False):
     nb, slots, pos = prompts(rng, bs, T)
     T = len(slots)
@@ -57,7 +67,7 @@ def run(rng, dtype, hq, hkv, d, bs, rot, il, T, want_heads, rope=True, in_place=
     qkv = rows(rng, dtype, T, hq + 2 * hkv, d, gain=2.0)
     qkv[5, hq:, 3] = np.inf
     qkv[9, hq:, 4] = np.nan
-    state = fp8_state(rng, nb, hkv, bs, d)
+    state = random_state(rng, nb, hkv, bs, d)
     kc, ks, vc, vs = f8(state[0]), dev(state[1]), f8(state[2]), dev(state[3])
     q, k, v = dev(qkv, dtype).split([hq, hkv, hkv], 1)
     pa.device_status(clear=True)
