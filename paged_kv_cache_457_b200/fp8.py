@@ -13,8 +13,8 @@ from .append import fp8_geometry, library, need_cuda, on_device, same_device, st
 
 PA_ERR_WORKSPACE = -7
 
-# Kept apart from the 16-bit calls' workspaces: a captured graph of those goes on using the one kept for its stream, which a
-# call here that needs more would free.
+# Kept apart from the 16-bit calls' workspaces: a captured graph of those goes on using the one kept for its stream, which
+# a call here that needs more would free.
 _workspaces: dict = {}
 
 
@@ -87,7 +87,8 @@ def decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
                max_context_len: int | None = None, out: torch.Tensor | None = None, partition_tokens: int = 0,
                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """:func:`decode` over an 8-bit cache: attention of q ([S, Hq, d], float16 or bfloat16) over each sequence's
-    context; returns out ([S, Hq, d], q's dtype).  Other arguments as :func:`decode`."""
+    context; returns out ([S, Hq, d], q's dtype).  Other arguments as :func:`decode`; ``partition_tokens`` is rounded
+    up to a multiple of 32, and to 64 at least."""
     dev = same_device(k_cache, q, v_cache, k_scale, v_scale, block_tables, context_lens)
     if dev is None:
         need_cuda(k_cache=k_cache, q=q, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
